@@ -1,4 +1,5 @@
-"""ctypes binding of libinjectstore.so (include/inject_store.h).
+"""ctypes binding of libinjectstore.so (include/inject_store.h,
+include/inject_query.h).
 
 Argument marshalling only: every step of the inject path runs in the CUDA
 library.  Pointers are plain integers (``tensor.data_ptr()``) and streams are
@@ -64,6 +65,19 @@ class is_ipc_handle_t(ctypes.Structure):
     _fields_ = [("bytes", ctypes.c_ubyte * 64)]
 
 
+class is_rows_t(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64), ("num_heads", _I32)]
+
+
+class is_attend_t(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _I32), ("num_requests", _I32), ("max_q_len", _I32), ("max_blocks_per_req", _I32),
+        ("q_offsets", _P), ("start_pos", _P), ("kv_lens", _P), ("block_tables", _P), ("shared_blocks", _P),
+        ("shared_len", _I32), ("causal", _I32), ("scale", ctypes.c_float), ("layer", _I32),
+        ("q", is_rows_t), ("out", is_rows_t), ("lse", _P),
+    ]
+
+
 class InjectError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -119,6 +133,18 @@ _SIGNATURES = {
     "is_inject_batch_noalloc": (ctypes.c_int, [ctypes.POINTER(is_store_config_t), _P, _P, _I64,
                                                _P, _P, _I32, _I32, _P, _P, _I32, _P, _P, _I32,
                                                ctypes.POINTER(is_cache_t), _P, _I64, _P, _P]),
+    "is_query_create": (ctypes.c_int, [ctypes.POINTER(is_store_config_t), ctypes.c_int, ctypes.POINTER(_P)]),
+    "is_query_destroy": (None, [_P]),
+    "is_query_last_error": (ctypes.c_int, [_P, _P, ctypes.POINTER(_I64)]),
+    "is_query_rotate": (ctypes.c_int, [_P, _I32, _P, ctypes.POINTER(is_rows_t), ctypes.POINTER(is_rows_t), _P,
+                                       ctypes.POINTER(is_rows_t), ctypes.POINTER(is_rows_t), _P, ctypes.c_float,
+                                       _P]),
+    "is_query_append": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.POINTER(is_rows_t), ctypes.POINTER(is_rows_t), _P,
+                                       ctypes.POINTER(is_rows_t), ctypes.POINTER(is_rows_t), _P, ctypes.c_float,
+                                       ctypes.POINTER(is_cache_t), _I32, _P]),
+    "is_query_attend_workspace": (ctypes.c_int, [_P, ctypes.POINTER(is_attend_t), ctypes.POINTER(is_cache_t),
+                                                 ctypes.POINTER(_I64)]),
+    "is_query_attend": (ctypes.c_int, [_P, ctypes.POINTER(is_attend_t), ctypes.POINTER(is_cache_t), _P, _I64, _P]),
 }
 for _name, (_res, _args) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
@@ -356,3 +382,49 @@ def is_inject_batch_noalloc(cfg: is_store_config_t, k_store: int, v_store: int,
                                         block_tables, max_blocks_per_req, ctypes.byref(cache),
                                         slot_mapping_out, slot_mapping_capacity, status_out,
                                         stream)
+
+
+# ---- the query side (include/inject_query.h) --------------------------------
+
+def is_query_create(cfg: is_store_config_t, device: int = 0) -> int:
+    out = _P()
+    check(_lib.is_query_create(ctypes.byref(cfg), device, ctypes.byref(out)), "is_query_create")
+    return out.value
+
+
+def is_query_destroy(query: int) -> None:
+    _lib.is_query_destroy(query)
+
+
+def is_query_last_error(query: int, stream: int = 0) -> tuple[int, int]:
+    detail = _I64()
+    rc = _lib.is_query_last_error(query, stream, ctypes.byref(detail))
+    return rc, detail.value
+
+
+def is_query_rotate(query: int, num_tokens: int, positions: int, q: is_rows_t, q_out: is_rows_t,
+                    q_weight: int | None, k: is_rows_t | None, k_out: is_rows_t | None, k_weight: int | None,
+                    eps: float, stream: int = 0) -> None:
+    """Asynchronous; raises on a host-side error."""
+    check(_lib.is_query_rotate(query, num_tokens, positions, q, q_out, q_weight, k, k_out, k_weight, eps, stream),
+          "is_query_rotate")
+
+
+def is_query_append(query: int, num_tokens: int, positions: int, slots: int, k: is_rows_t, v: is_rows_t,
+                    k_weight: int | None, q: is_rows_t | None, q_out: is_rows_t | None, q_weight: int | None,
+                    eps: float, cache: is_cache_t, layer: int, stream: int = 0) -> None:
+    """Asynchronous; raises on a host-side error."""
+    check(_lib.is_query_append(query, num_tokens, positions, slots, k, v, k_weight, q, q_out, q_weight, eps, cache,
+                               layer, stream), "is_query_append")
+
+
+def is_query_attend_workspace(query: int, args: is_attend_t, cache: is_cache_t) -> int:
+    out = _I64()
+    check(_lib.is_query_attend_workspace(query, args, cache, ctypes.byref(out)), "is_query_attend_workspace")
+    return out.value
+
+
+def is_query_attend(query: int, args: is_attend_t, cache: is_cache_t, workspace: int | None, workspace_bytes: int,
+                    stream: int = 0) -> None:
+    """Asynchronous; raises on a host-side error."""
+    check(_lib.is_query_attend(query, args, cache, workspace, workspace_bytes, stream), "is_query_attend")

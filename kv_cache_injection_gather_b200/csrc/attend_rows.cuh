@@ -1,0 +1,525 @@
+// Attention over the paged cache for few query rows per KV head (decode, a
+// few speculated tokens): the keys and values are read once and stream past
+// the rows, so HBM bandwidth bounds it.
+//
+//   s_j = scale q . k_j,  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+//
+// in one pass over the keys with the running maximum m and sum, in base 2
+// (scale * log2(e) is folded into one multiplier).  A tile of up to 16 rows
+// -- the (token, head) pairs of one request that share a KV head -- is the M
+// side of mma.m16n8k16 (bf16 in, fp32 out).  Each warp of a CTA walks its own
+// keys with its own cp.async ring, m, sum and accumulator, so the loop has no
+// CTA-wide barrier; the warps' parts are joined at the end.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "query_rows.cuh"
+
+namespace isq {
+
+struct AttendArgs {
+  int32_t num_tokens, num_requests, max_q_len, max_blocks;
+  const int32_t* q_offsets;
+  const int32_t* start_pos;
+  const int32_t* kv_lens;
+  const int32_t* block_tables;
+  const int32_t* shared_blocks;
+  int32_t shared_len;
+  int32_t causal;
+  float scale_log2;            // scale * log2(e)
+  int32_t num_heads;           // query heads
+  int32_t group;               // query heads per KV head
+  int32_t kv_heads;
+  Rows q, out;
+  float* lse;
+  // paged cache, at the layer
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  int64_t block_stride, token_stride, head_stride;
+  int32_t num_blocks, block_size;
+  Status* st;
+};
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __uint_as_float(0x7f800000u); }
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes global -> shared; `bytes` 16, or 0 to write zeros and read nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- requests
+
+struct Request {
+  int32_t tok0, n;      // its query tokens
+  int32_t start, kv;    // position of the first, keys in the cache
+};
+
+// Reads request r; 0, or the error that makes the batch skip it.
+__device__ __forceinline__ int32_t read_request(const AttendArgs& a, int32_t r, Request& q) {
+  const int32_t t0 = a.q_offsets[r], t1 = a.q_offsets[r + 1];
+  q.start = a.start_pos[r];
+  q.kv = a.kv_lens[r];
+  q.tok0 = t0;
+  q.n = t1 - t0;
+  if (t0 < 0 || t1 < t0 || t1 > a.num_tokens || q.n > a.max_q_len || q.start < 0 || q.kv < 0)
+    return kErrInvalidArg;
+  if (q.kv > a.shared_len && q.kv > int64_t(a.max_blocks) * a.block_size) return kErrPosition;
+  return 0;
+}
+
+// Position of query i of a request that is the first it does not see.
+__device__ __forceinline__ int32_t row_limit(const AttendArgs& a, const Request& q, int32_t i) {
+  if (!a.causal) return q.kv;
+  const int64_t lim = int64_t(q.start) + i + 1;
+  return lim < q.kv ? int32_t(lim) : q.kv;
+}
+
+// The request and row tile of work unit `unit`: the units are the requests'
+// tiles of ROWS rows (row = token * group + head), in order.  The whole CTA
+// calls this; r is -1 where there is no such unit.  Requests that read_request
+// refuses have no unit.
+template <int ROWS, int NT>
+__device__ __forceinline__ void find_unit(const AttendArgs& a, int32_t unit, int32_t& r, int32_t& tile, Request& q) {
+  if (int64_t(a.max_q_len) * a.group <= ROWS) {  // one tile each: the unit is the request
+    r = -1;
+    tile = 0;
+    if (unit < a.num_requests && read_request(a, unit, q) == 0 && q.n > 0) r = unit;
+    return;
+  }
+  __shared__ int32_t s_warp[NT / 32];
+  __shared__ int32_t s_found[6];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  if (tid == 0) s_found[0] = -1;
+  int32_t base = 0;
+  for (int32_t r0 = 0; r0 < a.num_requests; r0 += NT) {
+    Request mine;
+    int32_t tiles = 0;
+    if (r0 + tid < a.num_requests && read_request(a, r0 + tid, mine) == 0)
+      tiles = int32_t((int64_t(mine.n) * a.group + ROWS - 1) / ROWS);
+    int32_t upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    __syncthreads();  // s_warp of the round before is read
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    int32_t before = base, total = base;
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < warp) before += s_warp[i];
+      total += s_warp[i];
+    }
+    upto += before;
+    if (unit >= upto - tiles && unit < upto) {
+      s_found[0] = r0 + tid;
+      s_found[1] = unit - (upto - tiles);
+      s_found[2] = mine.tok0;
+      s_found[3] = mine.n;
+      s_found[4] = mine.start;
+      s_found[5] = mine.kv;
+    }
+    base = total;
+    if (unit < total) break;
+  }
+  __syncthreads();
+  r = s_found[0];
+  tile = s_found[1];
+  q.tok0 = s_found[2];
+  q.n = s_found[3];
+  q.start = s_found[4];
+  q.kv = s_found[5];
+}
+
+// Records the first refused request of the batch; one CTA of a grid does it.
+template <int NT>
+__device__ __forceinline__ void check_requests(const AttendArgs& a) {
+  __shared__ int32_t s_first;
+  if (threadIdx.x == 0) s_first = INT32_MAX;
+  __syncthreads();
+  Request q;
+  for (int32_t r = threadIdx.x; r < a.num_requests; r += NT)
+    if (read_request(a, r, q) != 0) {
+      atomicMin(&s_first, r);
+      break;
+    }
+  __syncthreads();
+  if (threadIdx.x == 0 && s_first != INT32_MAX) record(a.st, read_request(a, s_first, q), s_first);
+}
+
+// Block of position j (below the request's limit): the shared list's below
+// shared_len, the request's own otherwise; -1 if it lies outside the cache.
+__device__ __forceinline__ int32_t block_of(const AttendArgs& a, int32_t r, int32_t j, int32_t jb) {
+  const bool shared = j < a.shared_len;
+  const int32_t b = shared ? a.shared_blocks[jb] : a.block_tables[int64_t(r) * a.max_blocks + jb];
+  if (b >= 0 && b < a.num_blocks) return b;
+  record(a.st, kErrBadBlock, shared ? -1 : r);
+  return -1;
+}
+
+// Element offset of (position j, KV head h) in the layer's caches; -1 for a
+// bad block.
+__device__ __forceinline__ int64_t key_offset(const AttendArgs& a, int32_t r, int32_t h, int32_t j) {
+  const int32_t jb = j / a.block_size;
+  const int32_t b = block_of(a, r, j, jb);
+  if (b < 0) return -1;
+  return b * a.block_stride + int64_t(j - jb * a.block_size) * a.token_stride + h * a.head_stride;
+}
+
+// One row over keys [lo, hi) by a warp, key after key in fp32: for rows whose
+// tiled product came out infinite or NaN although keys that they do not see
+// may have caused it (0 * NaN).  o: dims lane, lane + 32, ...
+template <int D>
+__device__ __noinline__ void row_by_keys(const AttendArgs& a, int32_t r, int32_t h, const uint16_t* q, int32_t lo,
+                                         int32_t hi, float& m, float& l, float (&o)[D / 32]) {
+  const int lane = threadIdx.x & 31;
+  float x[D / 32];
+  m = neg_inf();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    x[i] = __uint_as_float(uint32_t(q[lane + 32 * i]) << 16);
+    o[i] = 0.f;
+  }
+  for (int32_t j = lo; j < hi; ++j) {
+    const int64_t at = key_offset(a, r, h, j);
+    if (at < 0) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      s = fmaf(x[i], __uint_as_float(uint32_t(a.k_cache[at + lane + 32 * i]) << 16), s);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+    s *= a.scale_log2;
+    const float top = fmaxf(m, s);
+    const float ref = top == neg_inf() ? 0.f : top;
+    const float shrink = exp2f(m - ref), p = exp2f(s - ref);
+    m = top;
+    l = l * shrink + p;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      o[i] = o[i] * shrink + p * __uint_as_float(uint32_t(a.v_cache[at + lane + 32 * i]) << 16);
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+constexpr int kTileRows = 16;
+
+template <int D>
+struct RowsShape {
+  static constexpr int kKeys = D <= 128 ? 32 : 16;       // keys of a warp's tile
+  static constexpr int kWarps = 4;
+  static constexpr int kStages = D <= 128 ? 3 : 3;
+  static constexpr int kTileBytes = kKeys * D * 2;        // K or V
+  static constexpr int kWarpBytes = kStages * 2 * kTileBytes;
+  static constexpr int kRingBytes = kWarps * kWarpBytes;
+  static constexpr int kQBytes = kTileRows * D * 2;
+  static constexpr int kSmemBytes = kRingBytes + kQBytes + 1024;
+};
+
+// Byte offset of 16-byte chunk c of row `row` in a [rows][D] bf16 tile, the
+// chunks permuted within groups of rows so that 8 consecutive rows at one
+// chunk (an ldmatrix phase) fall into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(int row, int c) {
+  constexpr int CPR = D / 8;
+  const int x = CPR >= 8 ? (row & 7) : ((row >> 1) & 3);
+  return uint32_t(row * CPR + (c ^ x)) * 16u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(RowsShape<D>::kWarps * 32) attend_rows_kernel(
+    const __grid_constant__ AttendArgs a) {
+  using S = RowsShape<D>;
+  constexpr int NT = S::kWarps * 32, TK = S::kKeys, CPR = D / 8, KS = D / 16, NK = TK / 8, ND = D / 8;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  unsigned char* ring = smem + warp * S::kWarpBytes;
+  unsigned char* q_tile = smem + S::kRingBytes;
+  __shared__ float s_m[S::kWarps][kTileRows], s_l[S::kWarps][kTileRows];
+  __shared__ int32_t s_odd[kTileRows];
+
+  const int32_t h = blockIdx.x % a.kv_heads;
+  const int32_t unit = blockIdx.x / a.kv_heads;
+  if (blockIdx.x == gridDim.x - 1) {  // a CTA of its own
+    check_requests<NT>(a);
+    return;
+  }
+  int32_t r, tile;
+  Request rq;
+  find_unit<kTileRows, NT>(a, unit, r, tile, rq);
+  if (r < 0) return;
+
+  const int32_t row0 = tile * kTileRows;
+  const int32_t rows = min(kTileRows, rq.n * a.group - row0);
+  auto token_of = [&](int row) { return (row0 + row) / a.group; };
+  auto head_of = [&](int row) { return h * a.group + (row0 + row) % a.group; };
+  const int32_t hi = row_limit(a, rq, token_of(rows - 1));  // the last row sees most
+  const int32_t lo = 0;
+
+  // ---- the queries, as the A operand of every product
+  for (int i = tid; i < kTileRows * CPR; i += NT) {
+    const int row = i / CPR, c = i % CPR;
+    const bool live = row < rows;
+    const uint16_t* src = a.q.data;
+    if (live) src += int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs + c * 8;
+    cp_async16(smem_addr(q_tile + tile_at<D>(row, c)), src, live ? 16 : 0);
+  }
+  cp_async_commit();
+
+  // ---- key tiles of this warp: tile i covers [lo + i * TK, ...), i = warp,
+  // warp + kWarps, ...
+  const int32_t tiles = (hi - lo + TK - 1) / TK;
+  uint32_t seen[S::kStages];  // keys of the stage that take part
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) seen[i] = 0;
+
+  auto load = [&](int32_t i, int stage) -> uint32_t {
+    const int32_t j = lo + i * TK + lane;
+    int64_t at = -1;
+    if (i < tiles && lane < TK && j < hi) at = key_offset(a, r, h, j);
+    const uint32_t ok = __ballot_sync(0xffffffffu, at >= 0);
+    if (i < tiles) {
+      const uint32_t k_dst = smem_addr(ring + stage * 2 * S::kTileBytes);
+#pragma unroll
+      for (int n = 0; n < TK * CPR / 32; ++n) {
+        const int e = n * 32 + lane, row = e / CPR, c = e % CPR;
+        const int64_t from = __shfl_sync(0xffffffffu, at, row);
+        const int64_t src = from < 0 ? 0 : from + c * 8;
+        const int bytes = from < 0 ? 0 : 16;
+        const uint32_t dst = k_dst + tile_at<D>(row, c);
+        cp_async16(dst, a.k_cache + src, bytes);
+        cp_async16(dst + S::kTileBytes, a.v_cache + src, bytes);
+      }
+    }
+    cp_async_commit();
+    return ok;
+  };
+
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) seen[s] = load(warp + s * S::kWarps, s);
+  cp_async_wait<S::kStages - 1>();  // the queries
+  __syncthreads();
+  uint32_t qf[KS][4];
+#pragma unroll
+  for (int k = 0; k < KS; ++k)
+    ldmatrix4(qf[k], smem_addr(q_tile + tile_at<D>(lane & 15, 2 * k + (lane >> 4))));
+
+  // rows lane / 4 and lane / 4 + 8 of the accumulators
+  const int ra = lane >> 2, rb = ra + 8;
+  const int32_t lim_a = ra < rows ? row_limit(a, rq, token_of(ra)) : hi;
+  const int32_t lim_b = rb < rows ? row_limit(a, rq, token_of(rb)) : hi;
+  const int32_t lim_min = row_limit(a, rq, token_of(0));
+  float m_a = neg_inf(), m_b = neg_inf(), l_a = 0.f, l_b = 0.f;
+  float o[ND][4];
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+  int stage = 0;
+  for (int32_t i = warp; i < tiles; i += S::kWarps) {
+    const int next = stage == 0 ? S::kStages - 1 : stage - 1;  // the stage read last
+    __syncwarp();
+    const uint32_t ahead = load(i + (S::kStages - 1) * S::kWarps, next);
+    uint32_t ok = 0;
+#pragma unroll
+    for (int s = 0; s < S::kStages; ++s) {
+      if (s == stage) ok = seen[s];
+      if (s == next) seen[s] = ahead;
+    }
+    cp_async_wait<S::kStages - 1>();
+    __syncwarp();
+    const unsigned char* kt = ring + stage * 2 * S::kTileBytes;
+    const unsigned char* vt = kt + S::kTileBytes;
+
+    float s[NK][4];
+#pragma unroll
+    for (int n = 0; n < NK; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int n = 0; n < NK; n += 2) {
+        uint32_t b[4];  // keys 8n .. 8n + 15, dims 16k .. 16k + 15
+        ldmatrix4(b, smem_addr(kt + tile_at<D>(n * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1))));
+        mma16816(s[n], qf[k], b[0], b[1]);
+        mma16816(s[n + 1], qf[k], b[2], b[3]);
+      }
+
+    const int32_t j0 = lo + i * TK;
+    constexpr uint32_t kAll = TK == 32 ? 0xffffffffu : (1u << TK) - 1u;
+    const bool whole = ok == kAll && j0 + TK <= lim_min;
+    float top_a = m_a, top_b = m_b;
+#pragma unroll
+    for (int n = 0; n < NK; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = s[n][e] * a.scale_log2;
+        if (!whole) {
+          const int col = n * 8 + (lane & 3) * 2 + (e & 1);
+          const bool in = ((ok >> col) & 1u) && j0 + col < (e < 2 ? lim_a : lim_b);
+          if (!in) x = neg_inf();
+        }
+        s[n][e] = x;
+        if (e < 2) top_a = fmaxf(top_a, x);
+        else top_b = fmaxf(top_b, x);
+      }
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+      top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, d));
+      top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, d));
+    }
+    // a row that has seen nothing yet: subtract 0, every term is 0
+    const float ref_a = top_a == neg_inf() ? 0.f : top_a, ref_b = top_b == neg_inf() ? 0.f : top_b;
+    const float shrink_a = exp2f(m_a - ref_a), shrink_b = exp2f(m_b - ref_b);
+    m_a = top_a;
+    m_b = top_b;
+    l_a *= shrink_a;
+    l_b *= shrink_b;
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = exp2f(s[n][e] - (e < 2 ? ref_a : ref_b));
+      l_a += s[n][0] + s[n][1];
+      l_b += s[n][2] + s[n][3];
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      o[d][0] *= shrink_a;
+      o[d][1] *= shrink_a;
+      o[d][2] *= shrink_b;
+      o[d][3] *= shrink_b;
+    }
+#pragma unroll
+    for (int k = 0; k < TK / 16; ++k) {
+      // the probabilities rounded to bf16: the products' other operand, V, is
+      // no finer, and the sum l keeps them in fp32
+      const uint32_t p[4] = {to_bf16x2(s[2 * k][0], s[2 * k][1]), to_bf16x2(s[2 * k][2], s[2 * k][3]),
+                             to_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]), to_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3])};
+#pragma unroll
+      for (int d = 0; d < ND; d += 2) {
+        uint32_t b[4];  // keys 16k .. 16k + 15, dims 8d .. 8d + 15
+        ldmatrix4_trans(b, smem_addr(vt + tile_at<D>(k * 16 + (lane & 15), d + (lane >> 4))));
+        mma16816(o[d], p, b[0], b[1]);
+        mma16816(o[d + 1], p, b[2], b[3]);
+      }
+    }
+    stage = stage == S::kStages - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+
+  // ---- join the warps' parts
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, d);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, d);
+  }
+  if ((lane & 3) == 0) {
+    s_m[warp][ra] = m_a;
+    s_m[warp][rb] = m_b;
+    s_l[warp][ra] = l_a;
+    s_l[warp][rb] = l_b;
+  }
+  if (tid < kTileRows) s_odd[tid] = 0;
+  __syncthreads();  // every ring is free
+  float* part = reinterpret_cast<float*>(smem);  // [warp][row][D]
+  static_assert(S::kWarps * kTileRows * D * 4 <= S::kRingBytes, "parts fit in the rings");
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    const int at = d * 8 + (lane & 3) * 2;
+    *reinterpret_cast<float2*>(part + (warp * kTileRows + ra) * D + at) = make_float2(o[d][0], o[d][1]);
+    *reinterpret_cast<float2*>(part + (warp * kTileRows + rb) * D + at) = make_float2(o[d][2], o[d][3]);
+  }
+  __syncthreads();
+  auto joined = [&](int row, float& m, float (&w)[S::kWarps]) -> float {
+    m = neg_inf();
+#pragma unroll
+    for (int k = 0; k < S::kWarps; ++k) m = fmaxf(m, s_m[k][row]);
+    const float ref = m == neg_inf() ? 0.f : m;
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::kWarps; ++k) {
+      w[k] = exp2f(s_m[k][row] - ref);
+      l += w[k] * s_l[k][row];
+    }
+    return l;
+  };
+  // in place: part of warp 0 becomes the row's sum
+  for (int i = tid; i < rows * (D / 4); i += NT) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    float m, w[S::kWarps];
+    const float l = joined(row, m, w);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < S::kWarps; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (k * kTileRows + row) * D + c * 4);
+      sum.x = fmaf(w[k], v.x, sum.x);
+      sum.y = fmaf(w[k], v.y, sum.y);
+      sum.z = fmaf(w[k], v.z, sum.z);
+      sum.w = fmaf(w[k], v.w, sum.w);
+    }
+    *reinterpret_cast<float4*>(part + row * D + c * 4) = sum;
+    if (!(finite(sum.x) && finite(sum.y) && finite(sum.z) && finite(sum.w) && finite(l))) s_odd[row] = 1;
+  }
+  __syncthreads();
+  for (int row = warp; row < rows; row += S::kWarps) {
+    const int32_t lim = row_limit(a, rq, token_of(row));
+    const int64_t t = rq.tok0 + token_of(row);
+    const int32_t head = head_of(row);
+    float m, w[S::kWarps];
+    float l = joined(row, m, w);
+    float x[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) x[i] = part[row * D + lane + 32 * i];
+    if (s_odd[row] && lim < hi)  // keys past the row's limit were in its tiles
+      row_by_keys<D>(a, r, h, a.q.data + t * a.q.ts + head * a.q.hs, lo, lim, m, l, x);
+    // a sum of 0: no key was seen, or none with a score above -inf
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      out[lane + 32 * i] = __bfloat16_as_ushort(__float2bfloat16_rn(none ? 0.f : x[i] * inv));
+    if (a.lse != nullptr && lane == 0)
+      a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
+  }
+}
+
+}  // namespace isq

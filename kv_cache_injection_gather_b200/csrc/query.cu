@@ -1,0 +1,320 @@
+// Host side of the query calls declared in include/inject_query.h: the
+// handle, the checks of arguments and the launches of the kernels in
+// query_rows.cuh and attend_rows.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "attend_rows.cuh"
+#include "inject_query.h"
+#include "query_rows.cuh"
+
+struct is_query {
+  int device = 0;
+  int sm_count = 148;
+  int32_t num_layers = 0, kv_heads = 0, head_dim = 0, style = 0;
+  double* turns = nullptr;  // [head_dim / 2] RoPE frequencies over 2 pi
+  isq::Status* status = nullptr;
+};
+
+namespace {
+
+struct OnDevice {
+  int prev = -1;
+  explicit OnDevice(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    if (prev != dev) cudaSetDevice(dev);
+    else prev = -1;
+  }
+  ~OnDevice() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+void free_query(is_query* q) {
+  if (!q) return;
+  cudaFree(q->turns);
+  cudaFree(q->status);
+  delete q;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Kernel tables over (head_dim, RoPE style) and head_dim.
+using RowsKernel = void (*)(isq::RowArgs);
+RowsKernel rows_kernel_of(int D, int style) {
+  switch (D) {
+    case 32: return style ? &isq::rows_kernel<32, 1> : &isq::rows_kernel<32, 0>;
+    case 64: return style ? &isq::rows_kernel<64, 1> : &isq::rows_kernel<64, 0>;
+    case 128: return style ? &isq::rows_kernel<128, 1> : &isq::rows_kernel<128, 0>;
+    case 256: return style ? &isq::rows_kernel<256, 1> : &isq::rows_kernel<256, 0>;
+    default: return nullptr;
+  }
+}
+
+struct AttendKernel {
+  void (*fn)(isq::AttendArgs);
+  int smem, threads;
+};
+template <int D>
+AttendKernel attend_rows_of() {
+  return {&isq::attend_rows_kernel<D>, isq::RowsShape<D>::kSmemBytes, isq::RowsShape<D>::kWarps * 32};
+}
+AttendKernel attend_rows_of(int D) {
+  switch (D) {
+    case 32: return attend_rows_of<32>();
+    case 64: return attend_rows_of<64>();
+    case 128: return attend_rows_of<128>();
+    default: return attend_rows_of<256>();
+  }
+}
+
+// Rows as the kernels take them; false where the header's rules are broken.
+bool rows_ok(const is_rows_t* r) {
+  return r && r->data && aligned16(r->data) && r->num_heads > 0 && r->token_stride >= 0 && r->head_stride >= 0 &&
+         r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+isq::Rows rows_of(const is_rows_t& r) {
+  return {static_cast<uint16_t*>(r.data), r.token_stride, r.head_stride};
+}
+
+bool cache_ok(const is_query* q, const is_cache_t* c, int32_t layer) {
+  return c && c->k_cache && c->v_cache && aligned16(c->k_cache) && aligned16(c->v_cache) && c->num_blocks > 0 &&
+         c->block_size >= 1 && c->block_size <= 128 && layer >= 0 && layer < q->num_layers && c->layer_stride >= 0 &&
+         c->block_stride >= 0 && c->token_stride >= 0 && c->head_stride >= 0 && c->layer_stride % 8 == 0 &&
+         c->block_stride % 8 == 0 && c->token_stride % 8 == 0 && c->head_stride % 8 == 0;
+}
+uint16_t* layer_of(void* cache, const is_cache_t* c, int32_t layer) {
+  return static_cast<uint16_t*>(cache) + int64_t(layer) * c->layer_stride;
+}
+
+int launch_rows(const is_query* q, const isq::RowArgs& a, int32_t num_tokens, cudaStream_t st) {
+  const int per_row = q->head_dim / 16;
+  const int64_t want = int64_t(a.nq + a.nk + a.nv) * per_row;
+  const int threads = int(std::min<int64_t>((want + 31) / 32 * 32, isq::kRowThreads));
+  rows_kernel_of(q->head_dim, q->style)<<<unsigned(num_tokens), unsigned(threads), 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
+}
+
+// The arguments of an attention call that do not need the device; IS_OK, or
+// the error.
+int check_attend(const is_query* q, const is_attend_t* a, const is_cache_t* c) {
+  if (!q || !a || !cache_ok(q, c, a->layer)) return IS_ERR_INVALID_ARG;
+  if (a->num_tokens < 0 || a->num_requests < 0 || a->max_q_len < 0 || a->max_blocks_per_req < 0 || a->shared_len < 0 ||
+      (a->causal != 0 && a->causal != 1) || !(a->scale >= 0.f) || !std::isfinite(a->scale))
+    return IS_ERR_INVALID_ARG;
+  if (a->q.num_heads <= 0 || a->q.num_heads % q->kv_heads != 0 || a->out.num_heads != a->q.num_heads)
+    return IS_ERR_INVALID_ARG;
+  if (a->num_tokens > 0 && a->num_requests > 0) {
+    if (!rows_ok(&a->q) || !rows_ok(&a->out) || !a->q_offsets || !a->start_pos || !a->kv_lens || a->max_q_len < 1 ||
+        (a->max_blocks_per_req > 0 && !a->block_tables) || (a->shared_len > 0 && !a->shared_blocks))
+      return IS_ERR_INVALID_ARG;
+  }
+  if (int64_t(a->num_tokens) * a->q.num_heads > INT32_MAX) return IS_ERR_CAPACITY;
+  return IS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) {
+  if (!cfg || !out) return IS_ERR_INVALID_ARG;
+  *out = nullptr;
+  const is_store_config_t& c = *cfg;
+  if (c.num_layers < 1 || c.num_kv_heads < 1 || !(c.rope_theta > 0) ||
+      (c.rope_style != IS_ROPE_ROTATE_HALF && c.rope_style != IS_ROPE_INTERLEAVED) ||
+      (c.rope_scaling != IS_SCALING_NONE && c.rope_scaling != IS_SCALING_LLAMA3))
+    return IS_ERR_INVALID_ARG;
+  if (c.rope_scaling == IS_SCALING_LLAMA3 &&
+      (!(c.scale_factor > 0) || !(c.low_freq_factor > 0) || !(c.high_freq_factor > c.low_freq_factor) ||
+       c.original_max_position < 1))
+    return IS_ERR_INVALID_ARG;
+  if (!rows_kernel_of(c.head_dim, 0)) return IS_ERR_NOT_SUPPORTED;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) {
+    cudaGetLastError();
+    return IS_ERR_CUDA;
+  }
+  OnDevice guard(device);
+  is_query* q = new (std::nothrow) is_query();
+  if (!q) return IS_ERR_OOM;
+  q->device = device;
+  q->num_layers = c.num_layers;
+  q->kv_heads = c.num_kv_heads;
+  q->head_dim = c.head_dim;
+  q->style = c.rope_style;
+  cudaDeviceGetAttribute(&q->sm_count, cudaDevAttrMultiProcessorCount, device);
+  if (cudaMalloc(reinterpret_cast<void**>(&q->turns), sizeof(double) * size_t(c.head_dim / 2)) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&q->status), sizeof(isq::Status)) != cudaSuccess) {
+    cudaGetLastError();
+    free_query(q);
+    return IS_ERR_OOM;
+  }
+  // Attributes now, so that the calls are launches alone (the functions are
+  // loaded here, not inside somebody's stream capture).
+  cudaFuncAttributes attr;
+  const AttendKernel ar = attend_rows_of(c.head_dim);
+  bool ok = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(rows_kernel_of(c.head_dim, c.rope_style))) ==
+                cudaSuccess &&
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(ar.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 ar.smem) == cudaSuccess;
+  ok = ok && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
+  isq::turns_kernel<<<(c.head_dim / 2 + 127) / 128, 128>>>(q->turns, c.head_dim, c.rope_theta, c.rope_scaling,
+                                                           c.scale_factor, c.low_freq_factor, c.high_freq_factor,
+                                                           double(c.original_max_position));
+  if (!ok || cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    free_query(q);
+    return IS_ERR_CUDA;
+  }
+  *out = q;
+  return IS_OK;
+}
+
+void is_query_destroy(is_query_t* q) {
+  if (!q) return;
+  OnDevice guard(q->device);
+  cudaDeviceSynchronize();
+  free_query(q);
+}
+
+int is_query_last_error(is_query_t* q, void* stream, int64_t* detail) {
+  if (!q) return IS_ERR_INVALID_ARG;
+  OnDevice guard(q->device);
+  isq::Status s{};
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      cudaMemcpy(&s, q->status, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return IS_ERR_CUDA;
+  if (s.code != 0 && cudaMemset(q->status, 0, sizeof(s)) != cudaSuccess) return IS_ERR_CUDA;
+  if (detail) *detail = s.detail;
+  return s.code;
+}
+
+int is_query_rotate(is_query_t* query, int32_t num_tokens, const int32_t* positions, const is_rows_t* q,
+                    const is_rows_t* q_out, const void* q_weight, const is_rows_t* k, const is_rows_t* k_out,
+                    const void* k_weight, float eps, void* stream) {
+  if (!query || num_tokens < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return IS_ERR_INVALID_ARG;
+  if (num_tokens == 0) return IS_OK;
+  if (!positions || !rows_ok(q) || !rows_ok(q_out) || q->num_heads != q_out->num_heads || !aligned16(q_weight) ||
+      !aligned16(k_weight) || (k == nullptr) != (k_out == nullptr))
+    return IS_ERR_INVALID_ARG;
+  if (k && (!rows_ok(k) || !rows_ok(k_out) || k->num_heads != k_out->num_heads)) return IS_ERR_INVALID_ARG;
+  OnDevice guard(query->device);
+  isq::RowArgs a{};
+  a.positions = positions;
+  a.nq = q->num_heads;
+  a.q = rows_of(*q);
+  a.q_out = rows_of(*q_out);
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  if (k) {
+    a.nk = k->num_heads;
+    a.k = rows_of(*k);
+    a.k_out = rows_of(*k_out);
+    a.k_weight = static_cast<const uint16_t*>(k_weight);
+  }
+  a.eps = eps;
+  a.turns = query->turns;
+  a.st = query->status;
+  return launch_rows(query, a, num_tokens, static_cast<cudaStream_t>(stream));
+}
+
+int is_query_append(is_query_t* query, int32_t num_tokens, const int32_t* positions, const int64_t* slots,
+                    const is_rows_t* k, const is_rows_t* v, const void* k_weight, const is_rows_t* q,
+                    const is_rows_t* q_out, const void* q_weight, float eps, const is_cache_t* cache, int32_t layer,
+                    void* stream) {
+  if (!query || num_tokens < 0 || !(eps >= 0.f) || !std::isfinite(eps) || !cache_ok(query, cache, layer))
+    return IS_ERR_INVALID_ARG;
+  if (num_tokens == 0) return IS_OK;
+  if (!positions || !slots || !rows_ok(k) || !rows_ok(v) || k->num_heads != query->kv_heads ||
+      v->num_heads != query->kv_heads || !aligned16(k_weight) || !aligned16(q_weight) ||
+      (q == nullptr) != (q_out == nullptr))
+    return IS_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q) || !rows_ok(q_out) || q->num_heads != q_out->num_heads)) return IS_ERR_INVALID_ARG;
+  OnDevice guard(query->device);
+  isq::RowArgs a{};
+  a.positions = positions;
+  a.slots = slots;
+  if (q) {
+    a.nq = q->num_heads;
+    a.q = rows_of(*q);
+    a.q_out = rows_of(*q_out);
+    a.q_weight = static_cast<const uint16_t*>(q_weight);
+  }
+  a.nk = a.nv = query->kv_heads;
+  a.k = rows_of(*k);
+  a.v = rows_of(*v);
+  a.k_weight = static_cast<const uint16_t*>(k_weight);
+  a.eps = eps;
+  a.turns = query->turns;
+  a.k_cache = layer_of(cache->k_cache, cache, layer);
+  a.v_cache = layer_of(cache->v_cache, cache, layer);
+  a.block_stride = cache->block_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.num_slots = int64_t(cache->num_blocks) * cache->block_size;
+  a.block_size = cache->block_size;
+  a.st = query->status;
+  return launch_rows(query, a, num_tokens, static_cast<cudaStream_t>(stream));
+}
+
+int is_query_attend_workspace(const is_query_t* query, const is_attend_t* args, const is_cache_t* cache,
+                              int64_t* bytes_out) {
+  if (!bytes_out) return IS_ERR_INVALID_ARG;
+  *bytes_out = 0;
+  return check_attend(query, args, cache);
+}
+
+int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t* cache, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+  const int rc = check_attend(query, args, cache);
+  if (rc != IS_OK) return rc;
+  if (args->num_tokens == 0 || args->num_requests == 0) return IS_OK;
+  (void)workspace;
+  (void)workspace_bytes;
+  OnDevice guard(query->device);
+  isq::AttendArgs a{};
+  a.num_tokens = args->num_tokens;
+  a.num_requests = args->num_requests;
+  a.max_q_len = std::min(args->max_q_len, args->num_tokens);
+  a.max_blocks = args->max_blocks_per_req;
+  a.q_offsets = args->q_offsets;
+  a.start_pos = args->start_pos;
+  a.kv_lens = args->kv_lens;
+  a.block_tables = args->block_tables;
+  a.shared_blocks = args->shared_blocks;
+  a.shared_len = args->shared_len;
+  a.causal = args->causal;
+  const double scale = args->scale > 0.f ? double(args->scale) : 1.0 / std::sqrt(double(query->head_dim));
+  a.scale_log2 = float(scale * 1.4426950408889634);
+  a.num_heads = args->q.num_heads;
+  a.kv_heads = query->kv_heads;
+  a.group = a.num_heads / a.kv_heads;
+  a.q = rows_of(args->q);
+  a.out = rows_of(args->out);
+  a.lse = args->lse;
+  a.k_cache = layer_of(cache->k_cache, cache, args->layer);
+  a.v_cache = layer_of(cache->v_cache, cache, args->layer);
+  a.block_stride = cache->block_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.st = query->status;
+
+  // one unit per request where a tile holds all its rows, else at most a
+  // partial tile per request more than the rows fill
+  const int64_t rows = int64_t(a.num_tokens) * a.group;
+  const int64_t units = int64_t(a.max_q_len) * a.group <= isq::kTileRows
+                            ? a.num_requests
+                            : (rows + isq::kTileRows - 1) / isq::kTileRows + a.num_requests;
+  const int64_t grid = units * a.kv_heads + 1;
+  if (grid > INT32_MAX) return IS_ERR_CAPACITY;
+  const AttendKernel k = attend_rows_of(query->head_dim);
+  k.fn<<<unsigned(grid), unsigned(k.threads), size_t(k.smem), static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
+}
+
+}  // extern "C"

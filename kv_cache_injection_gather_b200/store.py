@@ -26,6 +26,24 @@ def _i32(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
+def _rows(t: torch.Tensor, name: str, heads: int | None, D: int, T: int, device: int) -> B.is_rows_t:
+    """bf16 [T][heads][D] on the device, any strides but the innermost (1)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be bf16 [tokens][heads][{D}] with unit last stride")
+    n, h, d = t.shape
+    if n != T or d != D or (heads is not None and h != heads):
+        raise ValueError(f"{name} is {tuple(t.shape)}: expected ({T}, {'heads' if heads is None else heads}, {D})")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is not on cuda:{device}")
+    return B.is_rows_t(t.data_ptr(), t.stride(0), t.stride(1), h)
+
+
+def _ints(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: int) -> int:
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on cuda:{device}")
+    return t.data_ptr()
+
+
 class _DeviceArray:
     """__cuda_array_interface__ wrapper so torch can view library memory."""
 
@@ -76,9 +94,18 @@ class FactStore:
         self.device = device
         self.capacity_tokens = capacity_tokens
         self.handle = B.is_store_create(cfg, device)
+        self.query = None
+        try:
+            self.query = B.is_query_create(cfg, device)
+        except B.InjectError:
+            self.close()
+            raise
 
     # ---- lifetime
     def close(self) -> None:
+        if getattr(self, "query", None):
+            B.is_query_destroy(self.query)
+            self.query = None
         if getattr(self, "handle", None):
             B.is_store_destroy(self.handle)
             self.handle = None
@@ -261,3 +288,124 @@ class FactStore:
 
     def kernel_time(self) -> tuple[float, int]:
         return B.is_store_kernel_time(self.handle)
+
+    # ---- the query side
+    def _weight(self, w: torch.Tensor | None, name: str) -> int | None:
+        if w is None:
+            return None
+        if w.dtype is not torch.bfloat16 or w.dim() != 1 or w.shape[0] != self.D or not w.is_contiguous() \
+                or w.get_device() != self.device:
+            raise ValueError(f"{name} must be a contiguous bf16 [{self.D}] tensor on cuda:{self.device}")
+        return w.data_ptr()
+
+    def _stream(self, stream: int | None) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+
+    def _empty(self, shape, dtype: torch.dtype, stream: int | None) -> torch.Tensor:
+        """A new tensor whose memory belongs to the stream that writes it."""
+        dev = torch.device("cuda", self.device)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+    def rotate(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None,
+               q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+               q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+               stream: int | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+        """Queries and keys (bf16 [T][heads][D], strided slices allowed)
+        normed per head where a weight (bf16 [D]) is given, and rotated to
+        positions (int32 [T]; negative: a padding token, rows left alone).
+        Returns (q_out, k_out); an output may be its input.  Asynchronous."""
+        D, T, dev = self.D, q.shape[0], self.device
+        if q_out is None:
+            q_out = self._empty(q.shape, torch.bfloat16, stream)
+        qr = _rows(q, "q", None, D, T, dev)
+        qo = _rows(q_out, "q_out", qr.num_heads, D, T, dev)
+        kr = ko = None
+        if k is not None:
+            if k_out is None:
+                k_out = self._empty(k.shape, torch.bfloat16, stream)
+            kr = _rows(k, "k", None, D, T, dev)
+            ko = _rows(k_out, "k_out", kr.num_heads, D, T, dev)
+        elif k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight need k")
+        B.is_query_rotate(self.query, T, _ints(positions, "positions", T, torch.int32, dev), qr, qo,
+                          self._weight(q_weight, "q_weight"), kr, ko, self._weight(k_weight, "k_weight"), eps,
+                          self._stream(stream))
+        return q_out, k_out
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+               cache: B.is_cache_t, layer: int = 0, k_weight: torch.Tensor | None = None,
+               q: torch.Tensor | None = None, q_weight: torch.Tensor | None = None, eps: float = 1e-6,
+               q_out: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor | None:
+        """Write new tokens' keys (normed where k_weight is given, rotated to
+        positions) and values (bf16 [T][H][D]) to their slots (int64 [T], -1:
+        not stored) of one layer of the paged cache; q (optional) is rotated
+        in the same launch and returned in q_out.  Asynchronous."""
+        D, T, dev = self.D, k.shape[0], self.device
+        kr, vr = _rows(k, "k", self.H, D, T, dev), _rows(v, "v", self.H, D, T, dev)
+        qr = qo = None
+        if q is not None:
+            if q_out is None:
+                q_out = self._empty(q.shape, torch.bfloat16, stream)
+            qr = _rows(q, "q", None, D, T, dev)
+            qo = _rows(q_out, "q_out", qr.num_heads, D, T, dev)
+        elif q_out is not None or q_weight is not None:
+            raise ValueError("q_out and q_weight need q")
+        B.is_query_append(self.query, T, _ints(positions, "positions", T, torch.int32, dev),
+                          _ints(slots, "slots", T, torch.int64, dev), kr, vr, self._weight(k_weight, "k_weight"),
+                          qr, qo, self._weight(q_weight, "q_weight"), eps, cache, layer, self._stream(stream))
+        return q_out
+
+    def attend(self, q: torch.Tensor, q_offsets: torch.Tensor, start_pos: torch.Tensor, kv_lens: torch.Tensor,
+               block_tables: torch.Tensor, cache: B.is_cache_t, layer: int = 0, max_q_len: int | None = None,
+               shared_blocks: torch.Tensor | None = None, shared_len: int = 0, causal: bool = True,
+               scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               stream: int | None = None) -> torch.Tensor:
+        """Attention of query tokens over one layer of the paged cache.
+
+        q is bf16 [T][heads][D]; request r owns rows q_offsets[r] ..
+        q_offsets[r + 1], the first at position start_pos[r], and sees
+        kv_lens[r] cached positions (causal: up to its own) through its row of
+        block_tables -- positions below shared_len through shared_blocks,
+        which all requests share.  max_q_len bounds the requests' query
+        counts (1 for decode; default: T).  lse, if given, is fp32
+        [T][heads].  Asynchronous; last_query_error() has device-side errors."""
+        D, T, dev, R = self.D, q.shape[0], self.device, kv_lens.shape[0]
+        if out is None:
+            out = self._empty(q.shape, torch.bfloat16, stream)
+        if scale is not None and not scale > 0:
+            raise ValueError("scale must be positive")
+        i32 = torch.int32
+        if block_tables.dim() != 2 or block_tables.shape[0] != R or block_tables.dtype is not i32 \
+                or not block_tables.is_contiguous() or block_tables.get_device() != dev:
+            raise ValueError(f"block_tables must be a contiguous int32 [{R}][max_blocks] tensor on cuda:{dev}")
+        shared_ptr = None
+        if shared_len:
+            if shared_blocks is None or shared_blocks.numel() * cache.block_size < shared_len:
+                raise ValueError("shared_blocks does not cover shared_len")
+            shared_ptr = _ints(shared_blocks, "shared_blocks", shared_blocks.numel(), i32, dev)
+        lse_ptr = None
+        if lse is not None:
+            if lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() \
+                    or lse.get_device() != dev:
+                raise ValueError("lse must be a contiguous fp32 [tokens][heads] tensor on the device")
+            lse_ptr = lse.data_ptr()
+        qr = _rows(q, "q", None, D, T, dev)
+        args = B.is_attend_t(T, R, T if max_q_len is None else max_q_len, block_tables.shape[1],
+                             _ints(q_offsets, "q_offsets", R + 1, i32, dev),
+                             _ints(start_pos, "start_pos", R, i32, dev), _ints(kv_lens, "kv_lens", R, i32, dev),
+                             block_tables.data_ptr(), shared_ptr, shared_len, int(causal),
+                             0.0 if scale is None else scale, layer, qr,
+                             _rows(out, "out", qr.num_heads, D, T, dev), lse_ptr)
+        need = B.is_query_attend_workspace(self.query, args, cache)
+        work = self._empty((need,), torch.uint8, stream) if need else None
+        B.is_query_attend(self.query, args, cache, None if work is None else work.data_ptr(), need,
+                          self._stream(stream))
+        return out
+
+    def last_query_error(self, stream: int | None = None) -> tuple[int, int]:
+        """Waits for the stream; first device-side error of rotate, append
+        and attend since the previous call, and its detail."""
+        return B.is_query_last_error(self.query, self._stream(stream))
