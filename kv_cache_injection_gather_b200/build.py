@@ -18,6 +18,7 @@ _HEADERS = [os.path.join(ROOT, "include", "inject_store.h")]
 UNITS = {
     os.path.join(CSRC, "inject_store.cu"): [os.path.join(CSRC, "inject_kernels.cuh"), *_HEADERS],
     os.path.join(CSRC, "query.cu"): [os.path.join(CSRC, "query_rows.cuh"), os.path.join(CSRC, "attend_rows.cuh"),
+                                     os.path.join(CSRC, "attend_tiles.cuh"),
                                      os.path.join(ROOT, "include", "inject_query.h"), *_HEADERS],
 }
 SOURCES = list(UNITS)

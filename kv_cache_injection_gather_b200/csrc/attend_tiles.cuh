@@ -1,0 +1,534 @@
+// Attention over the paged cache for many query rows per KV head (prompts,
+// the query tokens of a request): the products bound it, so they run on the
+// fifth-generation tensor cores (tcgen05) with the scores and the output sum
+// in tensor memory.
+//
+// A CTA takes a unit of up to 256 rows -- (token, head) pairs of one request
+// that share a KV head -- and walks its keys in tiles of 128:
+//
+//   S = Q K^T (128 x 128, fp32 in tensor memory)
+//   P = exp2(scale S - m), rounded to bf16, over S in tensor memory
+//   O += P V
+//
+// Two streams keep the tensor cores busy while a stream's softmax runs.  A
+// unit of more than 128 rows gives each stream 128 rows and every key tile; a
+// smaller one gives both streams the same rows and every other key tile, and
+// their sums are joined at the end.
+//
+// Warps 0-3 and 4-7 do the streams' softmax, one row a thread; warps 8-11
+// gather keys and values from the cache's blocks into a ring of 128-key tiles
+// (16-byte cp.async into the 128-byte swizzle that the products read); one
+// thread of warp 12 issues the products.  mbarriers join them.  Every wait is
+// bounded: a thread that gives up sets a flag that all see, the CTA drains,
+// frees its tensor memory and records IS_ERR_TIMEOUT.
+#pragma once
+
+#include "attend_rows.cuh"
+
+namespace isq {
+
+enum : int32_t { kErrTimeout = -8 };
+
+constexpr int kStreamRows = 128;
+constexpr int kUnitRows = 2 * kStreamRows;
+constexpr int kTileKeys = 128;
+constexpr int kTilesThreads = 13 * 32;
+constexpr int kLoadThreads = 128;
+
+template <int D>
+struct TilesShape {
+  static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQBytes = kUnitRows * D * 2;
+  static constexpr int kSlabBytes = kTileKeys * 128;     // 64 dims of 128 rows
+  // data, and up to 1 KB to align it
+  static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
+};
+
+// ---------------------------------------------------------------- barriers
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Waits until the phase of the given parity has completed.  After the limit
+// (about two seconds), or once another thread has given up, returns false.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* failed) {
+  const uint32_t addr = smem_addr(bar);
+  const long long began = clock64();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*failed) return false;
+    if (clock64() - began > (1ll << 32)) {
+      *failed = 1;
+      return false;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The barrier gets one arrival when all products issued so far by this thread
+// are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle (layout 2), version 1.
+// lead: bytes between 64-element chunks of a transposed (key-major) operand;
+// stride: bytes between groups of 8 rows.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(lead >> 4) << 16) | (uint64_t(stride >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// Instruction descriptor: bf16 x bf16 -> fp32, M = 128.
+__host__ __device__ constexpr uint32_t product(int N, bool b_transposed) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_transposed ? 1u << 16 : 0u) | (uint32_t(N / 8) << 17) |
+         (uint32_t(kStreamRows / 16) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __grid_constant__ AttendArgs a) {
+  using S = TilesShape<D>;
+  constexpr int CPR = D / 8, NS = S::kSlots;
+  constexpr int kLag = NS - 2;  // copies in flight: the slots but the two being read
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_s[2], bar_p[2], bar_o;
+  __shared__ int64_t s_at[kTileKeys];
+  __shared__ uint32_t s_tmem;
+  __shared__ int32_t s_failed, s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+
+  if (blockIdx.x == gridDim.x - 1) {  // a CTA of its own
+    check_requests<kTilesThreads>(a);
+    return;
+  }
+  const int32_t h = blockIdx.x % a.kv_heads;
+  int32_t r, tile;
+  Request rq;
+  find_unit<kUnitRows, kTilesThreads>(a, blockIdx.x / a.kv_heads, r, tile, rq);
+  if (r < 0) return;
+
+  const int32_t row0 = tile * kUnitRows;
+  const int32_t rows = min(kUnitRows, rq.n * a.group - row0);
+  auto token_of = [&](int row) { return (row0 + row) / a.group; };
+  auto head_of = [&](int row) { return h * a.group + (row0 + row) % a.group; };
+  const int32_t lo = 0;
+  const int32_t hi = row_limit(a, rq, token_of(rows - 1));
+  const int32_t tiles = (hi - lo + kTileKeys - 1) / kTileKeys;
+  const bool by_rows = rows > kStreamRows;
+  const int32_t work = by_rows ? 2 * tiles : tiles;  // products S, streams in turn
+
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  unsigned char* ring = smem + S::kQBytes;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(&bar_full[i], kLoadThreads);
+      bar_init(&bar_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bar_s[i], 1);
+      bar_init(&bar_p[i], kStreamRows);
+    }
+    bar_init(&bar_o, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_failed = 0;
+    s_bad = 0;
+  }
+  if (warp == 12) tmem_alloc(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;  // S0 | S1 (128 columns each) | O0 | O1 (D each)
+  const uint32_t tmem_o = tmem + 256;
+  constexpr int OC = 128;        // columns between O0 and O1
+
+  float m = neg_inf(), l = 0.f;  // softmax warps: of this thread's row
+  int32_t lim = 0;
+
+  if (warp >= 8 && warp < 12) {
+    // ---------------- gather: Q, then tiles K0 V0 K1 V1 ...
+    const int x = tid - 8 * 32;
+    const uint32_t q_dst = smem_addr(smem);
+    for (int e = x; e < (by_rows ? kUnitRows : kStreamRows) * CPR; e += kLoadThreads) {
+      const int row = e / CPR, c = e % CPR;
+      const bool live = row < rows;
+      const uint16_t* src = a.q.data;
+      if (live) src += int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs + c * 8;
+      const int st = row / kStreamRows, rr = row % kStreamRows;
+      cp_async16(q_dst + st * S::kSlotBytes + (c / 8) * S::kSlabBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src,
+                 live ? 16 : 0);
+    }
+    auto landed = [&](int32_t u) {  // this thread's part of tile u, to the products
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(&bar_full[u % NS]);
+    };
+    const int32_t total = 2 * tiles;
+    bool ok = true;
+    int32_t u = 0;
+    for (; u < total && ok; ++u) {
+      const int slot = u % NS;
+      if (!(u & 1)) {  // offsets of the tile's keys, for K and V
+        const int32_t j = lo + (u >> 1) * kTileKeys + x;
+        int64_t at = -1;
+        if (j < hi) {
+          at = key_offset(a, r, h, j);
+          if (at < 0) s_bad = 1;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the tile before is read
+        s_at[x] = at;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      if (u >= NS) ok = bar_wait(&bar_empty[slot], ((u / NS) - 1) & 1, &s_failed);
+      const uint16_t* cache = (u & 1) ? a.v_cache : a.k_cache;
+      const uint32_t dst = smem_addr(ring + slot * S::kSlotBytes);
+      if (ok) {
+#pragma unroll
+        for (int n = 0; n < kTileKeys * CPR / kLoadThreads; ++n) {
+          const int e = n * kLoadThreads + x, row = e / CPR, c = e % CPR;
+          const int64_t at = s_at[row];
+          cp_async16(dst + (c / 8) * S::kSlabBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                     cache + (at < 0 ? 0 : at + c * 8), at < 0 ? 0 : 16);
+        }
+      }
+      cp_async_commit();
+      if (u >= kLag) {
+        cp_async_wait<kLag>();
+        landed(u - kLag);
+      }
+    }
+    cp_async_wait<0>();
+    if (ok)
+      for (int32_t v = max(0, total - kLag); v < total; ++v) landed(v);
+    // The named barrier above needs every thread: one that gives up makes the
+    // others give up at their next wait, but they may first pass it once more.
+    if (!ok && u < total) {
+      for (; u < total; ++u)
+        if (!(u & 1)) {
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+    }
+  } else if (warp == 12) {
+    // ---------------- products
+    if (lane == 0) {
+      bool ok = true;
+      auto tile_of = [&](int32_t w) { return by_rows ? w >> 1 : w; };
+      auto wait_tile = [&](int32_t u) { ok = ok && bar_wait(&bar_full[u % NS], (u / NS) & 1, &s_failed); };
+      auto scores = [&](int32_t w) {
+        const int st = w & 1, j = tile_of(w), slot = (2 * j) % NS;
+        wait_tile(2 * j);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t qa = smem_addr(smem) + (by_rows ? st * S::kSlotBytes : 0);
+        const uint32_t ka = smem_addr(ring + slot * S::kSlotBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k / 4) * S::kSlabBytes + (k % 4) * 32;
+          mma_ss(tmem + st * 128, operand(qa + at, 16, 1024), operand(ka + at, 16, 1024), product(kTileKeys, false),
+                 k > 0);
+        }
+        tc_commit(&bar_s[st]);
+        if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
+      };
+      if (work > 0) scores(0);
+      if (work > 1) scores(1);
+      for (int32_t w = 0; w < work && ok; ++w) {
+        const int st = w & 1, j = tile_of(w), slot = (2 * j + 1) % NS;
+        const bool first = by_rows ? j == 0 : j < 2;
+        ok = bar_wait(&bar_p[st], (w >> 1) & 1, &s_failed);
+        wait_tile(2 * j + 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t va = smem_addr(ring + slot * S::kSlotBytes);
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k)
+          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand(va + k * 2048, S::kSlabBytes, 1024),
+                 product(D, true), !first || k > 0);
+        if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
+        if (w + 2 < work) scores(w + 2);
+      }
+      tc_commit(&bar_o);
+      bar_wait(&bar_o, 0, &s_failed);  // nothing in flight beyond this point
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- softmax of stream st, one row a thread
+    const int st = warp / 4, row = (tid & 127) + (by_rows ? st * kStreamRows : 0);
+    lim = row < rows ? row_limit(a, rq, token_of(row)) : hi;
+    const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes a warp
+    const uint32_t ts = tmem + st * 128 + lanes, to = tmem_o + st * OC + lanes;
+    for (int32_t w = st; w < work; w += 2) {
+      // the whole warp goes on or stops: what follows is warp-wide
+      if (!__all_sync(0xffffffffu, bar_wait(&bar_s[st], (w >> 1) & 1, &s_failed))) break;
+      tc_fence_after();
+      const int32_t j0 = lo + (by_rows ? w >> 1 : w) * kTileKeys;
+      const bool masked = j0 + kTileKeys > lim_min;
+      const int32_t seen = lim - j0;  // columns below are seen
+      uint32_t v[32];
+      float top = neg_inf();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(ts + c * 32, v);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i < seen) top = fmaxf(top, __uint_as_float(v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+        }
+      }
+      top *= a.scale_log2;  // positive: the maximum's place is the same
+      // The reference m follows the maximum only when that has risen by more
+      // than 2^8: smaller steps leave P below 2^8 and O as it is.  All rows
+      // of a warp take part in a correction (factor 1 where none is needed).
+      float shrink = 1.f;
+      if (top > m + 8.f || (m == neg_inf() && top > m)) {
+        shrink = exp2_fast(m - top);
+        m = top;
+      }
+      // the products with V up to this stream's previous tile are done: the
+      // barrier's arrival followed them
+      if (w >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
+        l *= shrink;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          tmem_ld32(to + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * shrink);
+          tmem_st32(to + c * 32, v);
+        }
+      }
+      const float ref = m == neg_inf() ? 0.f : m;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(ts + c * 32, v);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i >= seen) v[i] = 0xff800000u;
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = exp2_fast(fmaf(__uint_as_float(v[2 * i]), a.scale_log2, -ref));
+          const float p1 = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), a.scale_log2, -ref));
+          sum[0] += p0;
+          sum[1] += p1;
+          p[i] = to_bf16x2(p0, p1);
+        }
+        tmem_st16(ts + c * 16, p);  // over scores that have been read
+      }
+      l += sum[0] + sum[1];
+      tmem_wait_st();
+      tc_fence_before();
+      bar_arrive(&bar_p[st]);
+    }
+  }
+
+  // ---------------- output
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool failed = s_failed != 0;
+  if (failed && tid == 0) record(a.st, kErrTimeout, r);
+  if (!failed && warp < 8) {
+    const int st = warp / 4;
+    const int rr = tid & 127;
+    const uint32_t to = tmem_o + st * OC + (uint32_t(warp & 3) << 21);
+    // joined sums of a row that both streams worked on: stream 1 hands its
+    // part over through the ring
+    float* part = reinterpret_cast<float*>(ring);  // [dim][row]
+    float* s_m = reinterpret_cast<float*>(smem);   // over the queries
+    float* s_l = s_m + kStreamRows;
+    float w0 = 1.f, w1 = 0.f;
+    const bool two = !by_rows && tiles > 1;
+    if (two) {
+      if (st == 1) {
+        s_m[rr] = m;
+        s_l[rr] = l;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(to + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[(c * 32 + i) * kStreamRows + rr] = __uint_as_float(v[i]);
+        }
+      }
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (st == 0) {
+        const float m1 = s_m[rr], l1 = s_l[rr];
+        const float top = fmaxf(m, m1), ref = top == neg_inf() ? 0.f : top;
+        w0 = exp2f(m - ref);
+        w1 = exp2f(m1 - ref);
+        l = l * w0 + l1 * w1;
+        m = top;
+      }
+    }
+    const int row = by_rows ? st * kStreamRows + rr : rr;
+    const bool mine = (by_rows || st == 0) && row < rows;
+    if (by_rows || st == 0) {
+      const int64_t t = rq.tok0 + token_of(mine ? row : 0);
+      const int32_t head = head_of(mine ? row : 0);
+      const bool none = l == 0.f || tiles == 0;
+      const float inv = none ? 0.f : 1.f / l;
+      uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
+      // A row is odd if keys past its limit, or a bad block, were among its
+      // tiles and its sums are not finite (or the block was bad): 0 * NaN.
+      const bool suspect = lim < hi || s_bad != 0;
+      bool odd = s_bad != 0;
+      if (tiles > 0) {
+        if (__any_sync(0xffffffffu, suspect && mine)) {
+          bool fine = finite(l);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(to + c * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x = __uint_as_float(v[i]) * w0;
+              if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
+              fine = fine && finite(x);
+            }
+          }
+          odd = odd || (suspect && !fine);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(to + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x = __uint_as_float(v[i]) * w0;
+            if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
+            v[i] = __float_as_uint(none ? 0.f : x * inv);
+          }
+          if (mine && !odd) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = to_bf16x2(__uint_as_float(v[i * 8 + 2 * e]), __uint_as_float(v[i * 8 + 2 * e + 1]));
+              st16(out + c * 32 + i * 8, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+          }
+        }
+      } else if (mine) {
+        for (int i = 0; i < CPR; ++i) st16(out + i * 8, make_uint4(0, 0, 0, 0));
+      }
+      if (mine && !odd && a.lse != nullptr)
+        a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
+      // odd rows, one after the other by the whole warp
+      uint32_t todo = __ballot_sync(0xffffffffu, odd && mine);
+      while (todo) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int64_t tt = __shfl_sync(0xffffffffu, t, from);
+        const int32_t hh = __shfl_sync(0xffffffffu, head, from), top = __shfl_sync(0xffffffffu, lim, from);
+        float om, ol, o[D / 32];
+        row_by_keys<D>(a, r, h, a.q.data + tt * a.q.ts + hh * a.q.hs, lo, top, om, ol, o);
+        const float scale = ol == 0.f ? 0.f : 1.f / ol;
+        uint16_t* dst = a.out.data + tt * a.out.ts + hh * a.out.hs;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          dst[lane + 32 * i] = __bfloat16_as_ushort(__float2bfloat16_rn(ol == 0.f ? 0.f : o[i] * scale));
+        if (lane == 0 && a.lse != nullptr)
+          a.lse[tt * a.num_heads + hh] = ol == 0.f ? neg_inf() : (om + log2f(ol)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+}  // namespace isq

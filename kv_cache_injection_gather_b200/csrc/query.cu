@@ -9,6 +9,7 @@
 #include <new>
 
 #include "attend_rows.cuh"
+#include "attend_tiles.cuh"
 #include "inject_query.h"
 #include "query_rows.cuh"
 
@@ -70,6 +71,17 @@ AttendKernel attend_rows_of(int D) {
     case 128: return attend_rows_of<128>();
     default: return attend_rows_of<256>();
   }
+}
+
+// The tensor-memory kernel: head_dim 64 and 128 (fn is nullptr otherwise).
+template <int D>
+AttendKernel attend_tiles_of() {
+  return {&isq::attend_tiles_kernel<D>, isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads};
+}
+AttendKernel attend_tiles_of(int D) {
+  if (D == 64) return attend_tiles_of<64>();
+  if (D == 128) return attend_tiles_of<128>();
+  return {nullptr, 0, 0};
 }
 
 // Rows as the kernels take them; false where the header's rules are broken.
@@ -162,6 +174,9 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
                 cudaSuccess &&
             cudaFuncSetAttribute(reinterpret_cast<const void*>(ar.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  ar.smem) == cudaSuccess;
+  const AttendKernel at = attend_tiles_of(c.head_dim);
+  ok = ok && (!at.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(at.fn),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, at.smem) == cudaSuccess);
   ok = ok && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
   isq::turns_kernel<<<(c.head_dim / 2 + 127) / 128, 128>>>(q->turns, c.head_dim, c.rope_theta, c.rope_scaling,
                                                            c.scale_factor, c.low_freq_factor, c.high_freq_factor,
@@ -304,15 +319,17 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   a.block_size = cache->block_size;
   a.st = query->status;
 
-  // one unit per request where a tile holds all its rows, else at most a
-  // partial tile per request more than the rows fill
-  const int64_t rows = int64_t(a.num_tokens) * a.group;
-  const int64_t units = int64_t(a.max_q_len) * a.group <= isq::kTileRows
-                            ? a.num_requests
-                            : (rows + isq::kTileRows - 1) / isq::kTileRows + a.num_requests;
+  const int64_t most = int64_t(a.max_q_len) * a.group;
+  const AttendKernel tiles = attend_tiles_of(query->head_dim);
+  const bool wide = tiles.fn && most > isq::kTileRows;
+  const AttendKernel k = wide ? tiles : attend_rows_of(query->head_dim);
+  const int32_t unit_rows = wide ? isq::kUnitRows : isq::kTileRows;
+  // one unit per request where it holds all the request's rows, else at most
+  // a partial unit per request more than the rows fill
+  const int64_t units = most <= unit_rows ? a.num_requests
+                                          : (int64_t(a.num_tokens) * a.group + unit_rows - 1) / unit_rows + a.num_requests;
   const int64_t grid = units * a.kv_heads + 1;
   if (grid > INT32_MAX) return IS_ERR_CAPACITY;
-  const AttendKernel k = attend_rows_of(query->head_dim);
   k.fn<<<unsigned(grid), unsigned(k.threads), size_t(k.smem), static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
 }
