@@ -29,6 +29,7 @@ struct AttendArgs {
   const int32_t* shared_blocks;
   int32_t shared_len;
   int32_t causal;
+  int32_t splits;              // rows kernel: CTAs (a cluster) that share a unit's keys
   float scale_log2;            // scale * log2(e)
   int32_t num_heads;           // query heads
   int32_t group;               // query heads per KV head
@@ -79,6 +80,36 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared variable in another CTA of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // ---------------------------------------------------------------- requests
@@ -181,23 +212,23 @@ __device__ __forceinline__ void check_requests(const AttendArgs& a) {
   if (threadIdx.x == 0 && s_first != INT32_MAX) record(a.st, read_request(a, s_first, q), s_first);
 }
 
-// Block of position j (below the request's limit): the shared list's below
-// shared_len, the request's own otherwise; -1 if it lies outside the cache.
-__device__ __forceinline__ int32_t block_of(const AttendArgs& a, int32_t r, int32_t j, int32_t jb) {
-  const bool shared = j < a.shared_len;
-  const int32_t b = shared ? a.shared_blocks[jb] : a.block_tables[int64_t(r) * a.max_blocks + jb];
-  if (b >= 0 && b < a.num_blocks) return b;
-  record(a.st, kErrBadBlock, shared ? -1 : r);
-  return -1;
-}
-
-// Element offset of (position j, KV head h) in the layer's caches; -1 for a
-// bad block.
-__device__ __forceinline__ int64_t key_offset(const AttendArgs& a, int32_t r, int32_t h, int32_t j) {
+// Table entry of position j (below the request's limit): the shared list's
+// below shared_len, the request's own otherwise.
+__device__ __forceinline__ int32_t table_entry(const AttendArgs& a, int32_t r, int32_t j) {
   const int32_t jb = j / a.block_size;
-  const int32_t b = block_of(a, r, j, jb);
-  if (b < 0) return -1;
-  return b * a.block_stride + int64_t(j - jb * a.block_size) * a.token_stride + h * a.head_stride;
+  return j < a.shared_len ? a.shared_blocks[jb] : a.block_tables[int64_t(r) * a.max_blocks + jb];
+}
+// Element offset of (position j in block `entry`, KV head h) in the layer's
+// caches; -1 for a block outside the cache, which is recorded.
+__device__ __forceinline__ int64_t entry_offset(const AttendArgs& a, int32_t r, int32_t h, int32_t j, int32_t entry) {
+  if (entry < 0 || entry >= a.num_blocks) {
+    record(a.st, kErrBadBlock, j < a.shared_len ? -1 : r);
+    return -1;
+  }
+  return entry * a.block_stride + int64_t(j % a.block_size) * a.token_stride + h * a.head_stride;
+}
+__device__ __forceinline__ int64_t key_offset(const AttendArgs& a, int32_t r, int32_t h, int32_t j) {
+  return entry_offset(a, r, h, j, table_entry(a, r, j));
 }
 
 // One row over keys [lo, hi) by a warp, key after key in fp32: for rows whose
@@ -272,25 +303,32 @@ __global__ void __launch_bounds__(RowsShape<D>::kWarps * 32) attend_rows_kernel(
   unsigned char* ring = smem + warp * S::kWarpBytes;
   unsigned char* q_tile = smem + S::kRingBytes;
   __shared__ float s_m[S::kWarps][kTileRows], s_l[S::kWarps][kTileRows];
+  __shared__ float s_cta_m[kTileRows], s_cta_l[kTileRows];
   __shared__ int32_t s_odd[kTileRows];
 
-  const int32_t h = blockIdx.x % a.kv_heads;
-  const int32_t unit = blockIdx.x / a.kv_heads;
-  if (blockIdx.x == gridDim.x - 1) {  // a CTA of its own
-    check_requests<NT>(a);
+  // grid: (unit, KV head, split), the splits of a unit and head a cluster; the
+  // cluster after the last checks the batch
+  const int32_t split = int32_t(blockIdx.x % a.splits);
+  const int32_t cluster = int32_t(blockIdx.x / a.splits);
+  const int32_t h = cluster % a.kv_heads;
+  if (cluster == gridDim.x / a.splits - 1) {
+    if (split == 0) check_requests<NT>(a);
     return;
   }
   int32_t r, tile;
   Request rq;
-  find_unit<kTileRows, NT>(a, unit, r, tile, rq);
-  if (r < 0) return;
+  find_unit<kTileRows, NT>(a, cluster / a.kv_heads, r, tile, rq);
+  if (r < 0) return;  // as the whole cluster does
 
   const int32_t row0 = tile * kTileRows;
   const int32_t rows = min(kTileRows, rq.n * a.group - row0);
   auto token_of = [&](int row) { return (row0 + row) / a.group; };
   auto head_of = [&](int row) { return h * a.group + (row0 + row) % a.group; };
-  const int32_t hi = row_limit(a, rq, token_of(rows - 1));  // the last row sees most
-  const int32_t lo = 0;
+  // keys [lo, hi) of this CTA, of all [0, last row's limit): whole tiles
+  const int32_t all = row_limit(a, rq, token_of(rows - 1));
+  const int64_t all_tiles = (all + TK - 1) / TK;
+  const int32_t lo = int32_t(all_tiles * split / a.splits) * TK;
+  const int32_t hi = min(all, int32_t(all_tiles * (split + 1) / a.splits) * TK);
 
   // ---- the queries, as the A operand of every product
   for (int i = tid; i < kTileRows * CPR; i += NT) {
@@ -304,16 +342,24 @@ __global__ void __launch_bounds__(RowsShape<D>::kWarps * 32) attend_rows_kernel(
 
   // ---- key tiles of this warp: tile i covers [lo + i * TK, ...), i = warp,
   // warp + kWarps, ...
-  const int32_t tiles = (hi - lo + TK - 1) / TK;
+  const int32_t tiles = hi > lo ? (hi - lo + TK - 1) / TK : 0;
   uint32_t seen[S::kStages];  // keys of the stage that take part
 #pragma unroll
   for (int i = 0; i < S::kStages; ++i) seen[i] = 0;
+  // A lane's key of a tile and its table entry, read one tile ahead of the
+  // loads that need it.
+  auto key_of = [&](int32_t i) -> int32_t {
+    const int64_t j = lo + int64_t(i) * TK + lane;
+    return i < tiles && lane < TK && j < hi ? int32_t(j) : -1;
+  };
+  int32_t next_key = key_of(warp);
+  int32_t next_entry = next_key < 0 ? 0 : table_entry(a, r, next_key);
 
   auto load = [&](int32_t i, int stage) -> uint32_t {
-    const int32_t j = lo + i * TK + lane;
-    int64_t at = -1;
-    if (i < tiles && lane < TK && j < hi) at = key_offset(a, r, h, j);
+    const int64_t at = next_key < 0 ? -1 : entry_offset(a, r, h, next_key, next_entry);
     const uint32_t ok = __ballot_sync(0xffffffffu, at >= 0);
+    next_key = key_of(i + S::kWarps);
+    next_entry = next_key < 0 ? 0 : table_entry(a, r, next_key);
     if (i < tiles) {
       const uint32_t k_dst = smem_addr(ring + stage * 2 * S::kTileBytes);
 #pragma unroll
@@ -468,58 +514,81 @@ __global__ void __launch_bounds__(RowsShape<D>::kWarps * 32) attend_rows_kernel(
     *reinterpret_cast<float2*>(part + (warp * kTileRows + rb) * D + at) = make_float2(o[d][2], o[d][3]);
   }
   __syncthreads();
-  auto joined = [&](int row, float& m, float (&w)[S::kWarps]) -> float {
-    m = neg_inf();
+  // the CTA's sums take the place of warp 0's part
+  for (int i = tid; i < rows * (D / 4); i += NT) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    float m = neg_inf();
 #pragma unroll
     for (int k = 0; k < S::kWarps; ++k) m = fmaxf(m, s_m[k][row]);
     const float ref = m == neg_inf() ? 0.f : m;
     float l = 0.f;
-#pragma unroll
-    for (int k = 0; k < S::kWarps; ++k) {
-      w[k] = exp2f(s_m[k][row] - ref);
-      l += w[k] * s_l[k][row];
-    }
-    return l;
-  };
-  // in place: part of warp 0 becomes the row's sum
-  for (int i = tid; i < rows * (D / 4); i += NT) {
-    const int row = i / (D / 4), c = i % (D / 4);
-    float m, w[S::kWarps];
-    const float l = joined(row, m, w);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < S::kWarps; ++k) {
+      const float w = exp2f(s_m[k][row] - ref);
+      l += w * s_l[k][row];
       const float4 v = *reinterpret_cast<const float4*>(part + (k * kTileRows + row) * D + c * 4);
-      sum.x = fmaf(w[k], v.x, sum.x);
-      sum.y = fmaf(w[k], v.y, sum.y);
-      sum.z = fmaf(w[k], v.z, sum.z);
-      sum.w = fmaf(w[k], v.w, sum.w);
+      sum.x = fmaf(w, v.x, sum.x);
+      sum.y = fmaf(w, v.y, sum.y);
+      sum.z = fmaf(w, v.z, sum.z);
+      sum.w = fmaf(w, v.w, sum.w);
     }
     *reinterpret_cast<float4*>(part + row * D + c * 4) = sum;
+    if (c == 0) {
+      s_cta_m[row] = m;
+      s_cta_l[row] = l;
+    }
     if (!(finite(sum.x) && finite(sum.y) && finite(sum.z) && finite(sum.w) && finite(l))) s_odd[row] = 1;
   }
   __syncthreads();
   for (int row = warp; row < rows; row += S::kWarps) {
     const int32_t lim = row_limit(a, rq, token_of(row));
-    const int64_t t = rq.tok0 + token_of(row);
-    const int32_t head = head_of(row);
-    float m, w[S::kWarps];
-    float l = joined(row, m, w);
-    float x[D / 32];
+    if (!s_odd[row] || lim >= hi) continue;
+    // keys past the row's limit were in its tiles
+    float m, l, x[D / 32];
+    row_by_keys<D>(a, r, h, a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs, lo, lim, m, l,
+                   x);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = part[row * D + lane + 32 * i];
-    if (s_odd[row] && lim < hi)  // keys past the row's limit were in its tiles
-      row_by_keys<D>(a, r, h, a.q.data + t * a.q.ts + head * a.q.hs, lo, lim, m, l, x);
+    for (int i = 0; i < D / 32; ++i) part[row * D + lane + 32 * i] = x[i];
+    if (lane == 0) {
+      s_cta_m[row] = m;
+      s_cta_l[row] = l;
+    }
+  }
+
+  // ---- join the splits' sums: each CTA of the cluster a share of the rows'
+  // vectors, read from all of them
+  if (a.splits > 1) cluster_sync();
+  else __syncthreads();
+  const uint32_t part_at = smem_addr(part), m_at = smem_addr(s_cta_m), l_at = smem_addr(s_cta_l);
+  for (int i = split * NT + tid; i < rows * (D / 4); i += NT * a.splits) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    float m = neg_inf();
+    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, ld_cluster(in_cta(m_at + row * 4, k)));
+    const float ref = m == neg_inf() ? 0.f : m;
+    float l = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < a.splits; ++k) {
+      const float w = exp2f(ld_cluster(in_cta(m_at + row * 4, k)) - ref);
+      l += w * ld_cluster(in_cta(l_at + row * 4, k));
+      const float4 v = ld_cluster4(in_cta(part_at + (row * D + c * 4) * 4, k));
+      sum.x = fmaf(w, v.x, sum.x);
+      sum.y = fmaf(w, v.y, sum.y);
+      sum.z = fmaf(w, v.z, sum.z);
+      sum.w = fmaf(w, v.w, sum.w);
+    }
     // a sum of 0: no key was seen, or none with a score above -inf
     const bool none = l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
-    uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      out[lane + 32 * i] = __bfloat16_as_ushort(__float2bfloat16_rn(none ? 0.f : x[i] * inv));
-    if (a.lse != nullptr && lane == 0)
+    const int64_t t = rq.tok0 + token_of(row);
+    const int32_t head = head_of(row);
+    if (none) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<uint2*>(a.out.data + t * a.out.ts + head * a.out.hs + c * 4) =
+        make_uint2(to_bf16x2(sum.x * inv, sum.y * inv), to_bf16x2(sum.z * inv, sum.w * inv));
+    if (a.lse != nullptr && c == 0)
       a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
   }
+  if (a.splits > 1) cluster_sync();  // no CTA leaves while another reads it
 }
 
 }  // namespace isq

@@ -84,6 +84,13 @@ AttendKernel attend_tiles_of(int D) {
   return {nullptr, 0, 0};
 }
 
+// Rows of a KV head and request up to which the keys are streamed past 16-row
+// tiles (attend_rows) instead of 128-row ones (attend_tiles).
+constexpr int kMostNarrowRows = 64;
+// Splits of a unit's keys, and the keys that a split should at least have.
+constexpr int kMostSplits = 8;
+constexpr int kKeysPerSplit = 128;
+
 // Rows as the kernels take them; false where the header's rules are broken.
 bool rows_ok(const is_rows_t* r) {
   return r && r->data && aligned16(r->data) && r->num_heads > 0 && r->token_stride >= 0 && r->head_stride >= 0 &&
@@ -321,17 +328,38 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
 
   const int64_t most = int64_t(a.max_q_len) * a.group;
   const AttendKernel tiles = attend_tiles_of(query->head_dim);
-  const bool wide = tiles.fn && most > isq::kTileRows;
+  const bool wide = tiles.fn && most > kMostNarrowRows;
   const AttendKernel k = wide ? tiles : attend_rows_of(query->head_dim);
   const int32_t unit_rows = wide ? isq::kUnitRows : isq::kTileRows;
   // one unit per request where it holds all the request's rows, else at most
   // a partial unit per request more than the rows fill
   const int64_t units = most <= unit_rows ? a.num_requests
                                           : (int64_t(a.num_tokens) * a.group + unit_rows - 1) / unit_rows + a.num_requests;
-  const int64_t grid = units * a.kv_heads + 1;
+  // The keys of a unit are split over a cluster while the grid leaves SMs
+  // idle and a split keeps some tiles per warp.
+  a.splits = 1;
+  const int64_t keys = std::min<int64_t>(INT32_MAX, std::max<int64_t>(int64_t(a.max_blocks) * a.block_size, a.shared_len));
+  if (!wide)
+    while (a.splits < kMostSplits && units * a.kv_heads * a.splits < 2 * query->sm_count &&
+           keys >= int64_t(2 * a.splits) * kKeysPerSplit)
+      a.splits *= 2;
+  const int64_t grid = (units * a.kv_heads + 1) * a.splits;
   if (grid > INT32_MAX) return IS_ERR_CAPACITY;
-  k.fn<<<unsigned(grid), unsigned(k.threads), size_t(k.smem), static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(k.threads));
+  cfg.dynamicSmemBytes = size_t(k.smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {unsigned(a.splits), 1, 1};
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k.fn, a) != cudaSuccess) {
+    cudaGetLastError();
+    return IS_ERR_CUDA;
+  }
+  return IS_OK;
 }
 
 }  // extern "C"
