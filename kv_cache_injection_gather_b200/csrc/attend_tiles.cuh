@@ -17,8 +17,8 @@
 //
 // Warps 0-3 and 4-7 do the streams' softmax, one row a thread; warps 8-11
 // gather keys and values from the cache's blocks into a ring of 128-key tiles
-// (16-byte cp.async into the 128-byte swizzle that the products read); one
-// thread of warp 12 issues the products.  mbarriers join them.  Every wait is
+// (TMA boxes of a block's tokens, in the 128-byte swizzle that the products
+// read); one thread of warp 12 issues the products.  mbarriers join them.  Every wait is
 // bounded: a thread that gives up sets a flag that all see, the CTA drains,
 // frees its tensor memory and records IS_ERR_TIMEOUT.
 #pragma once
@@ -26,8 +26,6 @@
 #include "attend_rows.cuh"
 
 namespace isq {
-
-enum : int32_t { kErrTimeout = -8 };
 
 constexpr int kStreamRows = 128;
 constexpr int kUnitRows = 2 * kStreamRows;
@@ -44,35 +42,6 @@ struct TilesShape {
   // data, and up to 1 KB to align it
   static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
 };
-
-// ---------------------------------------------------------------- barriers
-
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-// Waits until the phase of the given parity has completed.  After the limit
-// (about two seconds), or once another thread has given up, returns false.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* failed) {
-  const uint32_t addr = smem_addr(bar);
-  const long long began = clock64();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*failed) return false;
-    if (clock64() - began > (1ll << 32)) {
-      *failed = 1;
-      return false;
-    }
-  }
-}
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -154,43 +123,79 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ---------------------------------------------------------------- the kernel
 
-template <int D>
-__global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __grid_constant__ AttendArgs a) {
+// The request that owns query token t: the last r with q_offsets[r] <= t.
+__device__ __forceinline__ int32_t owner_of(const AttendArgs& a, int32_t t) {
+  int32_t at = 0, n = a.num_requests;
+  while (n > 1) {
+    const int32_t half = n / 2;
+    if (a.q_offsets[at + half] <= t) {
+      at += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return at;
+}
+
+// SHARED: the units are 256 rows of all requests' query tokens, and their keys
+// those of the shared prefix; otherwise rows and keys of one request.  Where
+// a.part_o is set, split s of a unit's keys goes to part s of the work space;
+// otherwise there is one split and it goes to the output.
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
+    const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
+    const __grid_constant__ CUtensorMap v_map) {
   using S = TilesShape<D>;
   constexpr int CPR = D / 8, NS = S::kSlots;
-  constexpr int kLag = NS - 2;  // copies in flight: the slots but the two being read
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_s[2], bar_p[2], bar_o;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o;
   __shared__ int64_t s_at[kTileKeys];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
-  if (blockIdx.x == gridDim.x - 1) {  // a CTA of its own
-    check_requests<kTilesThreads>(a);
-    return;
-  }
-  const int32_t h = blockIdx.x % a.kv_heads;
+  let_next_start();
+  // grid: (unit, KV head, split), and a CTA that checks the batch (in SHARED
+  // the grid that follows does)
+  const int32_t split = int32_t(blockIdx.x % a.splits);
+  const int32_t h = int32_t(blockIdx.x / a.splits) % a.kv_heads;
+  const int32_t unit = int32_t(blockIdx.x / a.splits) / a.kv_heads;
   int32_t r, tile;
   Request rq;
-  find_unit<kUnitRows, kTilesThreads>(a, blockIdx.x / a.kv_heads, r, tile, rq);
-  if (r < 0) return;
+  if constexpr (SHARED) {
+    r = -1;
+    tile = unit;
+    rq = {0, a.num_tokens, 0, 0};
+  } else {
+    if (blockIdx.x == gridDim.x - 1) {
+      check_requests<kTilesThreads>(a);
+      return;
+    }
+    find_unit<kUnitRows, kTilesThreads>(a, unit, r, tile, rq);
+    if (r < 0) return;
+  }
 
   const int32_t row0 = tile * kUnitRows;
-  const int32_t rows = min(kUnitRows, rq.n * a.group - row0);
+  const int32_t rows = int32_t(min(int64_t(kUnitRows), int64_t(rq.n) * a.group - row0));
   auto token_of = [&](int row) { return (row0 + row) / a.group; };
   auto head_of = [&](int row) { return h * a.group + (row0 + row) % a.group; };
-  const int32_t lo = 0;
-  const int32_t hi = row_limit(a, rq, token_of(rows - 1));
-  const int32_t tiles = (hi - lo + kTileKeys - 1) / kTileKeys;
+  // First key that a row does not see.
+  auto limit_of = [&](int row) -> int32_t {
+    if constexpr (!SHARED) return row_limit(a, rq, token_of(row));
+    const int32_t t = token_of(row), o = owner_of(a, t);
+    Request q;
+    if (read_request(a, o, q) != 0 || t < q.tok0 || t >= q.tok0 + q.n) return 0;
+    return row_limit(a, q, t - q.tok0);
+  };
+  // keys [lo, hi) of this CTA: whole tiles but the last
+  const int32_t all = SHARED ? a.shared_len : limit_of(rows - 1);
+  const int64_t all_tiles = (int64_t(all) + kTileKeys - 1) / kTileKeys;
+  const int32_t lo = int32_t(all_tiles * split / a.splits) * kTileKeys;
+  const int32_t hi = int32_t(min(int64_t(all), all_tiles * (split + 1) / a.splits * kTileKeys));
+  const int32_t tiles = hi > lo ? (hi - lo + kTileKeys - 1) / kTileKeys : 0;
   const bool by_rows = rows > kStreamRows;
   const int32_t work = by_rows ? 2 * tiles : tiles;  // products S, streams in turn
 
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
       bar_init(&bar_s[i], 1);
       bar_init(&bar_p[i], kStreamRows);
     }
+    bar_init(&bar_q, kLoadThreads);
     bar_init(&bar_o, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_failed = 0;
@@ -232,59 +238,92 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
       const uint16_t* src = a.q.data;
       if (live) src += int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs + c * 8;
       const int st = row / kStreamRows, rr = row % kStreamRows;
-      cp_async16(q_dst + st * S::kSlotBytes + (c / 8) * S::kSlabBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), src,
-                 live ? 16 : 0);
+      cp_async16(q_dst + st * S::kSlotBytes + tile_at<D>(kStreamRows, rr, c), src, live ? 16 : 0);
     }
-    auto landed = [&](int32_t u) {  // this thread's part of tile u, to the products
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(&bar_full[u % NS]);
+    cp_async_commit();
+    auto q_landed = [&] {
+      cp_async_wait<0>();
+      proxy_fence();
+      bar_arrive(&bar_q);
     };
+    if (x == 0) {
+      fetch_map(&k_map);
+      fetch_map(&v_map);
+    }
+    // A tile comes as boxes (op = lane of the first warp: box lane / SL, slab
+    // lane % SL), or key by key: where a box holds keys of two blocks, where
+    // there is no map, and for values that run past hi, whose rows from there
+    // on have to be zeros.
+    constexpr int SL = D / 64;
+    const int32_t box_bits = max(0, a.box_log2), my_box = lane / SL << box_bits;
+    auto by_box = [&](int32_t j0, bool v) {
+      const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys &&
+                        (a.table_shared & ((1 << box_bits) - 1)) != 0;
+      return a.box_log2 >= 0 && !torn && !(v && hi - j0 < kTileKeys);
+    };
+    auto position = [&](int32_t t) -> int32_t {  // that this lane looks up for tile t as boxes
+      return t < tiles && my_box < kTileKeys && hi - (lo + t * kTileKeys) > my_box ? lo + t * kTileKeys + my_box : -1;
+    };
+    int32_t pos = -1, entry = 0, next_pos = position(0);
+    int32_t next_entry = next_pos < 0 || a.box_log2 < 0 ? 0 : table_entry(a, r, next_pos);
     const int32_t total = 2 * tiles;
-    bool ok = true;
-    int32_t u = 0;
-    for (; u < total && ok; ++u) {
+    for (int32_t u = 0; u < total; ++u) {
       const int slot = u % NS;
-      if (!(u & 1)) {  // offsets of the tile's keys, for K and V
-        const int32_t j = lo + (u >> 1) * kTileKeys + x;
+      const bool v = u & 1;
+      const int32_t j0 = lo + (u >> 1) * kTileKeys;
+      if (!v) {
+        pos = next_pos;
+        entry = next_entry;
+        next_pos = position((u >> 1) + 1);  // read a tile ahead of the copies that need it
+        if (next_pos >= 0 && a.box_log2 >= 0) next_entry = table_entry(a, r, next_pos);
+      }
+      // after a wait that gave up the loop runs out without copies
+      const bool ok = u < NS || bar_wait(&bar_empty[slot], ((u / NS) - 1) & 1, &s_failed);
+      const uint32_t dst = smem_addr(ring + slot * S::kSlotBytes);
+      if (by_box(j0, v)) {
+        if (warp == 8) {
+          const bool good = ok && pos >= 0 && entry >= 0 && entry < a.num_blocks;
+          if (pos >= 0 && !(entry >= 0 && entry < a.num_blocks)) {
+            record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
+            s_bad = 1;
+          }
+          const uint32_t ops = __ballot_sync(0xffffffffu, good);
+          if (lane == 0) bar_expect(&bar_full[slot], (uint32_t(__popc(ops)) << box_bits) * 128);
+          else bar_arrive(&bar_full[slot]);
+          if (good)
+            copy_box(dst + lane % SL * S::kSlabBytes + my_box * 128, v ? &v_map : &k_map, lane % SL * 64,
+                     pos % a.block_size, entry, h, &bar_full[slot]);
+        } else {
+          bar_arrive(&bar_full[slot]);
+        }
+      } else {
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // s_at of the tile before is read
         int64_t at = -1;
-        if (j < hi) {
-          at = key_offset(a, r, h, j);
+        if (hi - j0 > x) {
+          at = key_offset(a, r, h, j0 + x);
           if (at < 0) s_bad = 1;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the tile before is read
         s_at[x] = at;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-      }
-      if (u >= NS) ok = bar_wait(&bar_empty[slot], ((u / NS) - 1) & 1, &s_failed);
-      const uint16_t* cache = (u & 1) ? a.v_cache : a.k_cache;
-      const uint32_t dst = smem_addr(ring + slot * S::kSlotBytes);
-      if (ok) {
-#pragma unroll
-        for (int n = 0; n < kTileKeys * CPR / kLoadThreads; ++n) {
-          const int e = n * kLoadThreads + x, row = e / CPR, c = e % CPR;
-          const int64_t at = s_at[row];
-          cp_async16(dst + (c / 8) * S::kSlabBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                     cache + (at < 0 ? 0 : at + c * 8), at < 0 ? 0 : 16);
+        const uint16_t* cache = v ? a.v_cache : a.k_cache;
+        if (ok) {
+#pragma unroll 4
+          for (int n = 0; n < kTileKeys * CPR / kLoadThreads; ++n) {
+            const int e = n * kLoadThreads + x, row = e / CPR, c = e % CPR;
+            const int64_t from = s_at[row];
+            cp_async16(dst + tile_at<D>(kTileKeys, row, c), cache + (from < 0 ? 0 : from + c * 8), from < 0 ? 0 : 16);
+          }
         }
+        cp_async_commit();
+        cp_async_wait<0>();
+        proxy_fence();
+        bar_arrive(&bar_full[slot]);
       }
-      cp_async_commit();
-      if (u >= kLag) {
-        cp_async_wait<kLag>();
-        landed(u - kLag);
-      }
+      if (u == min(total, NS) - 1) q_landed();  // the ring is full of copies by now
     }
     cp_async_wait<0>();
-    if (ok)
-      for (int32_t v = max(0, total - kLag); v < total; ++v) landed(v);
-    // The named barrier above needs every thread: one that gives up makes the
-    // others give up at their next wait, but they may first pass it once more.
-    if (!ok && u < total) {
-      for (; u < total; ++u)
-        if (!(u & 1)) {
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-    }
+    if (*static_cast<volatile int32_t*>(&s_failed))  // copies in flight: nothing may leave before they land
+      for (int32_t u = max(0, total - NS); u < total; ++u) bar_wait(&bar_full[u % NS], (u / NS) & 1, nullptr);
   } else if (warp == 12) {
     // ---------------- products
     if (lane == 0) {
@@ -307,6 +346,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
         tc_commit(&bar_s[st]);
         if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
       };
+      if (work > 0) ok = bar_wait(&bar_q, 0, &s_failed);
       if (work > 0) scores(0);
       if (work > 1) scores(1);
       for (int32_t w = 0; w < work && ok; ++w) {
@@ -325,13 +365,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
         if (w + 2 < work) scores(w + 2);
       }
       tc_commit(&bar_o);
-      bar_wait(&bar_o, 0, &s_failed);  // nothing in flight beyond this point
+      bar_wait(&bar_o, 0, nullptr);  // nothing in flight beyond this point
     }
     __syncwarp();
   } else if (warp < 8) {
     // ---------------- softmax of stream st, one row a thread
     const int st = warp / 4, row = (tid & 127) + (by_rows ? st * kStreamRows : 0);
-    lim = row < rows ? row_limit(a, rq, token_of(row)) : hi;
+    lim = row < rows ? min(hi, limit_of(row)) : hi;
     const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes a warp
     const uint32_t ts = tmem + st * 128 + lanes, to = tmem_o + st * OC + lanes;
@@ -413,7 +453,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
   __syncthreads();
   tc_fence_after();
   const bool failed = s_failed != 0;
-  if (failed && tid == 0) record(a.st, kErrTimeout, r);
+  if (failed && tid == 0) record(a.st, kErrTimeout, unit);
   if (!failed && warp < 8) {
     const int st = warp / 4;
     const int rr = tid & 127;
@@ -456,6 +496,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
       const bool none = l == 0.f || tiles == 0;
       const float inv = none ? 0.f : 1.f / l;
       uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
+      const int64_t part_row = (int64_t(split) * a.num_tokens + t) * a.num_heads + head;
+      const bool to_part = a.part_o != nullptr;
       // A row is odd if keys past its limit, or a bad block, were among its
       // tiles and its sums are not finite (or the block was bad): 0 * NaN.
       const bool suspect = lim < hi || s_bad != 0;
@@ -486,9 +528,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
           for (int i = 0; i < 32; ++i) {
             float x = __uint_as_float(v[i]) * w0;
             if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
-            v[i] = __float_as_uint(none ? 0.f : x * inv);
+            v[i] = __float_as_uint(to_part ? x : none ? 0.f : x * inv);
           }
-          if (mine && !odd) {
+          if (mine && !odd && to_part) {
+            float* dst = a.part_o + part_row * D + c * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (mine && !odd) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t o[4];
@@ -499,10 +546,12 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
             }
           }
         }
-      } else if (mine) {
+      } else if (mine && !to_part) {
         for (int i = 0; i < CPR; ++i) st16(out + i * 8, make_uint4(0, 0, 0, 0));
       }
-      if (mine && !odd && a.lse != nullptr)
+      if (mine && !odd && to_part)
+        a.part_ml[part_row] = make_float2(m, l);
+      else if (mine && !odd && a.lse != nullptr)
         a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
       // odd rows, one after the other by the whole warp
       uint32_t todo = __ballot_sync(0xffffffffu, odd && mine);
@@ -513,6 +562,13 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(const __
         const int32_t hh = __shfl_sync(0xffffffffu, head, from), top = __shfl_sync(0xffffffffu, lim, from);
         float om, ol, o[D / 32];
         row_by_keys<D>(a, r, h, a.q.data + tt * a.q.ts + hh * a.q.hs, lo, top, om, ol, o);
+        if (to_part) {
+          const int64_t at = (int64_t(split) * a.num_tokens + tt) * a.num_heads + hh;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) a.part_o[at * D + lane + 32 * i] = o[i];
+          if (lane == 0) a.part_ml[at] = make_float2(om, ol);
+          continue;
+        }
         const float scale = ol == 0.f ? 0.f : 1.f / ol;
         uint16_t* dst = a.out.data + tt * a.out.ts + hh * a.out.hs;
 #pragma unroll

@@ -1,7 +1,9 @@
 // Host side of the query calls declared in include/inject_query.h: the
 // handle, the checks of arguments and the launches of the kernels in
 // query_rows.cuh and attend_rows.cuh.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
@@ -19,6 +21,7 @@ struct is_query {
   int32_t num_layers = 0, kv_heads = 0, head_dim = 0, style = 0;
   double* turns = nullptr;  // [head_dim / 2] RoPE frequencies over 2 pi
   isq::Status* status = nullptr;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;  // the driver's
 };
 
 namespace {
@@ -57,12 +60,12 @@ RowsKernel rows_kernel_of(int D, int style) {
 }
 
 struct AttendKernel {
-  void (*fn)(isq::AttendArgs);
-  int smem, threads;
+  void (*fn)(isq::AttendArgs, CUtensorMap, CUtensorMap);
+  int smem, threads, keys;  // keys of a tile
 };
 template <int D>
 AttendKernel attend_rows_of() {
-  return {&isq::attend_rows_kernel<D>, isq::RowsShape<D>::kSmemBytes, isq::RowsShape<D>::kWarps * 32};
+  return {&isq::attend_rows_kernel<D>, isq::RowsShape<D>::kSmemBytes, isq::RowsShape<D>::kWarps * 32, isq::RowsShape<D>::kKeys};
 }
 AttendKernel attend_rows_of(int D) {
   switch (D) {
@@ -75,21 +78,69 @@ AttendKernel attend_rows_of(int D) {
 
 // The tensor-memory kernel: head_dim 64 and 128 (fn is nullptr otherwise).
 template <int D>
-AttendKernel attend_tiles_of() {
-  return {&isq::attend_tiles_kernel<D>, isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads};
+AttendKernel attend_tiles_of(bool shared) {
+  return {shared ? &isq::attend_tiles_kernel<D, true> : &isq::attend_tiles_kernel<D, false>,
+          isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads, isq::kTileKeys};
 }
-AttendKernel attend_tiles_of(int D) {
-  if (D == 64) return attend_tiles_of<64>();
-  if (D == 128) return attend_tiles_of<128>();
-  return {nullptr, 0, 0};
+AttendKernel attend_tiles_of(int D, bool shared) {
+  if (D == 64) return attend_tiles_of<64>(shared);
+  if (D == 128) return attend_tiles_of<128>(shared);
+  return {nullptr, 0, 0, 0};
 }
 
 // Rows of a KV head and request up to which the keys are streamed past 16-row
 // tiles (attend_rows) instead of 128-row ones (attend_tiles).
 constexpr int kMostNarrowRows = 64;
-// Splits of a unit's keys, and the keys that a split should at least have.
+// Splits of a unit's keys in a cluster, and the keys that a split should at
+// least have.
 constexpr int kMostSplits = 8;
 constexpr int kKeysPerSplit = 128;
+// The shared prefix gets a grid of its own (attend_tiles over all requests'
+// rows) where the requests would otherwise read this many bytes of it.
+constexpr int64_t kSharedBytes = 64 << 20;
+constexpr int kMostParts = 16;
+
+// What an attention call launches; all from the host's numbers.
+struct AttendPlan {
+  bool wide;             // attend_tiles over requests, else attend_rows
+  int64_t units;         // of the requests' grid
+  int32_t splits;        // its splits (attend_rows: a cluster)
+  int32_t parts;         // splits of the shared prefix's grid; 0: no such grid
+  int64_t shared_units;
+  int64_t ml_bytes, o_bytes;  // work space
+};
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t* c) {
+  AttendPlan p{};
+  const int64_t group = a->q.num_heads / q->kv_heads;
+  const int64_t rows = int64_t(a->num_tokens) * group;
+  const int64_t most = int64_t(std::min(a->max_q_len, a->num_tokens)) * group;
+  const bool has_tiles = attend_tiles_of(q->head_dim, false).fn != nullptr;
+  p.wide = has_tiles && most > kMostNarrowRows;
+  const int64_t unit_rows = p.wide ? isq::kUnitRows : isq::kTileRows;
+  // one unit per request where it holds all the request's rows, else at most
+  // a partial unit per request more than the rows fill
+  p.units = most <= unit_rows ? a->num_requests : (rows + unit_rows - 1) / unit_rows + a->num_requests;
+  if (has_tiles && !p.wide && a->num_requests > 1 && int64_t(a->shared_len) * a->num_requests * q->kv_heads * q->head_dim * 4 >= kSharedBytes) {
+    p.shared_units = (rows + isq::kUnitRows - 1) / isq::kUnitRows;
+    const int64_t ctas = p.shared_units * q->kv_heads, tiles = (int64_t(a->shared_len) + 127) / 128;
+    p.parts = int32_t(std::max<int64_t>(1, std::min<int64_t>({q->sm_count / ctas, (tiles + 1) / 2, kMostParts})));
+    p.ml_bytes = round256(int64_t(p.parts) * a->num_tokens * a->q.num_heads * int64_t(sizeof(float2)));
+    p.o_bytes = int64_t(p.parts) * a->num_tokens * a->q.num_heads * q->head_dim * int64_t(sizeof(float));
+  }
+  // The keys of a unit are split over a cluster while the grid leaves SMs
+  // idle and a split keeps some tiles per warp.
+  p.splits = 1;
+  const int64_t keys = std::max<int64_t>(int64_t(a->max_blocks_per_req) * c->block_size, a->shared_len) -
+                       (p.parts ? a->shared_len : 0);
+  if (!p.wide)
+    while (p.splits < kMostSplits && p.units * q->kv_heads * p.splits < 2 * q->sm_count &&
+           keys >= int64_t(2 * p.splits) * kKeysPerSplit)
+      p.splits *= 2;
+  return p;
+}
 
 // Rows as the kernels take them; false where the header's rules are broken.
 bool rows_ok(const is_rows_t* r) {
@@ -108,6 +159,29 @@ bool cache_ok(const is_query* q, const is_cache_t* c, int32_t layer) {
 }
 uint16_t* layer_of(void* cache, const is_cache_t* c, int32_t layer) {
   return static_cast<uint16_t*>(cache) + int64_t(layer) * c->layer_stride;
+}
+
+// Tensor maps of a layer's K and V for a kernel's tiles: [D][B][blocks][heads]
+// with the cache's strides, in boxes of 64 dims (32 for D = 32) x the largest
+// power of two of tokens that divides the block and the tile.  Returns that
+// power's logarithm, or -1 where no box of 8 tokens fits or the cache's
+// strides have no map (the kernels then gather key by key).
+int box_maps(const is_query* q, const isq::AttendArgs& a, int tile_keys, CUtensorMap& k, CUtensorMap& v) {
+  int box = 0;
+  while ((2 << box) <= tile_keys && a.block_size % (2 << box) == 0) ++box;
+  if (box < 3 || !q->encode) return -1;
+  const int D = q->head_dim, slab = std::min(D, 64);
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(a.block_size), cuuint64_t(a.num_blocks), cuuint64_t(a.kv_heads)};
+  const cuuint64_t strides[3] = {cuuint64_t(a.token_stride) * 2, cuuint64_t(a.block_stride) * 2,
+                                 cuuint64_t(a.head_stride) * 2};
+  const cuuint32_t boxes[4] = {cuuint32_t(slab), cuuint32_t(1 << box), 1, 1}, ones[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle swizzle = slab == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  for (int i = 0; i < 2; ++i)
+    if (q->encode(i ? &v : &k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(i ? a.v_cache : a.k_cache), dims,
+                  strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return -1;
+  return box;
 }
 
 int launch_rows(const is_query* q, const isq::RowArgs& a, int32_t num_tokens, cudaStream_t st) {
@@ -181,10 +255,18 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
                 cudaSuccess &&
             cudaFuncSetAttribute(reinterpret_cast<const void*>(ar.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  ar.smem) == cudaSuccess;
-  const AttendKernel at = attend_tiles_of(c.head_dim);
-  ok = ok && (!at.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(at.fn),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, at.smem) == cudaSuccess);
-  ok = ok && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
+  for (bool shared : {false, true}) {
+    const AttendKernel at = attend_tiles_of(c.head_dim, shared);
+    ok = ok && (!at.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(at.fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, at.smem) == cudaSuccess);
+  }
+  void* encode = nullptr;
+  cudaDriverEntryPointQueryResult found{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &encode, 12000, cudaEnableDefault, &found) ==
+          cudaSuccess &&
+      found == cudaDriverEntryPointSuccess)
+    q->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode);
+  ok = ok && q->encode && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
   isq::turns_kernel<<<(c.head_dim / 2 + 127) / 128, 128>>>(q->turns, c.head_dim, c.rope_theta, c.rope_scaling,
                                                            c.scale_factor, c.low_freq_factor, c.high_freq_factor,
                                                            double(c.original_max_position));
@@ -286,7 +368,13 @@ int is_query_attend_workspace(const is_query_t* query, const is_attend_t* args, 
                               int64_t* bytes_out) {
   if (!bytes_out) return IS_ERR_INVALID_ARG;
   *bytes_out = 0;
-  return check_attend(query, args, cache);
+  const int rc = check_attend(query, args, cache);
+  if (rc != IS_OK) return rc;
+  if (args->num_tokens > 0 && args->num_requests > 0) {
+    const AttendPlan p = plan_attend(query, args, cache);
+    *bytes_out = p.ml_bytes + p.o_bytes;
+  }
+  return IS_OK;
 }
 
 int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t* cache, void* workspace,
@@ -294,8 +382,14 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   const int rc = check_attend(query, args, cache);
   if (rc != IS_OK) return rc;
   if (args->num_tokens == 0 || args->num_requests == 0) return IS_OK;
-  (void)workspace;
-  (void)workspace_bytes;
+  const AttendPlan p = plan_attend(query, args, cache);
+  if (p.ml_bytes + p.o_bytes > 0) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return IS_ERR_INVALID_ARG;
+    if (workspace_bytes < p.ml_bytes + p.o_bytes) return IS_ERR_CAPACITY;
+  }
+  const int64_t grid = (p.units * query->kv_heads + 1) * p.splits;
+  const int64_t shared_grid = p.shared_units * query->kv_heads * p.parts;
+  if (grid > INT32_MAX || shared_grid > INT32_MAX) return IS_ERR_CAPACITY;
   OnDevice guard(query->device);
   isq::AttendArgs a{};
   a.num_tokens = args->num_tokens;
@@ -307,7 +401,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   a.kv_lens = args->kv_lens;
   a.block_tables = args->block_tables;
   a.shared_blocks = args->shared_blocks;
-  a.shared_len = args->shared_len;
+  a.shared_len = a.table_shared = args->shared_len;
   a.causal = args->causal;
   const double scale = args->scale > 0.f ? double(args->scale) : 1.0 / std::sqrt(double(query->head_dim));
   a.scale_log2 = float(scale * 1.4426950408889634);
@@ -326,36 +420,43 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   a.block_size = cache->block_size;
   a.st = query->status;
 
-  const int64_t most = int64_t(a.max_q_len) * a.group;
-  const AttendKernel tiles = attend_tiles_of(query->head_dim);
-  const bool wide = tiles.fn && most > kMostNarrowRows;
-  const AttendKernel k = wide ? tiles : attend_rows_of(query->head_dim);
-  const int32_t unit_rows = wide ? isq::kUnitRows : isq::kTileRows;
-  // one unit per request where it holds all the request's rows, else at most
-  // a partial unit per request more than the rows fill
-  const int64_t units = most <= unit_rows ? a.num_requests
-                                          : (int64_t(a.num_tokens) * a.group + unit_rows - 1) / unit_rows + a.num_requests;
-  // The keys of a unit are split over a cluster while the grid leaves SMs
-  // idle and a split keeps some tiles per warp.
-  a.splits = 1;
-  const int64_t keys = std::min<int64_t>(INT32_MAX, std::max<int64_t>(int64_t(a.max_blocks) * a.block_size, a.shared_len));
-  if (!wide)
-    while (a.splits < kMostSplits && units * a.kv_heads * a.splits < 2 * query->sm_count &&
-           keys >= int64_t(2 * a.splits) * kKeysPerSplit)
-      a.splits *= 2;
-  const int64_t grid = (units * a.kv_heads + 1) * a.splits;
-  if (grid > INT32_MAX) return IS_ERR_CAPACITY;
+  CUtensorMap k_map{}, v_map{};
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  if (p.parts) {
+    isq::AttendArgs sa = a;
+    sa.splits = p.parts;
+    sa.part_ml = a.part_ml = static_cast<float2*>(workspace);
+    sa.part_o = a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
+    const AttendKernel k = attend_tiles_of(query->head_dim, true);
+    sa.box_log2 = box_maps(query, sa, k.keys, k_map, v_map);
+    cfg.gridDim = dim3(unsigned(shared_grid));
+    cfg.blockDim = dim3(unsigned(k.threads));
+    cfg.dynamicSmemBytes = size_t(k.smem);
+    if (cudaLaunchKernelEx(&cfg, k.fn, sa, k_map, v_map) != cudaSuccess) {
+      cudaGetLastError();
+      return IS_ERR_CUDA;
+    }
+    // the requests' grid starts beside it and waits for the parts at its end
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    a.num_parts = p.parts;
+    a.first_key = a.shared_len;
+    a.table_shared = 0;  // what is left of a request is in its own blocks
+  }
+  a.splits = p.splits;
+  if (!p.wide && p.splits > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.splits), 1, 1};
+  }
+  const AttendKernel k = p.wide ? attend_tiles_of(query->head_dim, false) : attend_rows_of(query->head_dim);
+  a.box_log2 = box_maps(query, a, k.keys, k_map, v_map);
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(k.threads));
   cfg.dynamicSmemBytes = size_t(k.smem);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {unsigned(a.splits), 1, 1};
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, k.fn, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k.fn, a, k_map, v_map) != cudaSuccess) {
     cudaGetLastError();
     return IS_ERR_CUDA;
   }

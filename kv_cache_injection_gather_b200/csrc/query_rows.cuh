@@ -19,6 +19,7 @@ enum : int32_t {
   kErrInvalidArg = -1,
   kErrPosition = -3,
   kErrBadBlock = -4,
+  kErrTimeout = -8,
 };
 
 struct Status {
