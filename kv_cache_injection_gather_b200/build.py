@@ -17,8 +17,8 @@ _HEADERS = [os.path.join(ROOT, "include", "inject_store.h")]
 # its own, side by side, and linked into the one library
 UNITS = {
     os.path.join(CSRC, "inject_store.cu"): [os.path.join(CSRC, "inject_kernels.cuh"), *_HEADERS],
-    os.path.join(CSRC, "query.cu"): [os.path.join(CSRC, "query_rows.cuh"), os.path.join(CSRC, "attend_rows.cuh"),
-                                     os.path.join(CSRC, "attend_tiles.cuh"),
+    os.path.join(CSRC, "query.cu"): [os.path.join(CSRC, "query_rows.cuh"), os.path.join(CSRC, "attend_common.cuh"),
+                                     os.path.join(CSRC, "attend_rows.cuh"), os.path.join(CSRC, "attend_tiles.cuh"),
                                      os.path.join(ROOT, "include", "inject_query.h"), *_HEADERS],
 }
 SOURCES = list(UNITS)

@@ -23,13 +23,12 @@
 // frees its tensor memory and records IS_ERR_TIMEOUT.
 #pragma once
 
-#include "attend_rows.cuh"
+#include "attend_common.cuh"
 
 namespace isq {
 
 constexpr int kStreamRows = 128;
 constexpr int kUnitRows = 2 * kStreamRows;
-constexpr int kTileKeys = 128;
 constexpr int kTilesThreads = 13 * 32;
 constexpr int kLoadThreads = 128;
 
@@ -42,86 +41,6 @@ struct TilesShape {
   // data, and up to 1 KB to align it
   static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
 };
-
-// ---------------------------------------------------------------- tcgen05
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// The barrier gets one arrival when all products issued so far by this thread
-// are done.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory operand descriptor, 128-byte swizzle (layout 2), version 1.
-// lead: bytes between 64-element chunks of a transposed (key-major) operand;
-// stride: bytes between groups of 8 rows.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(lead >> 4) << 16) | (uint64_t(stride >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// Instruction descriptor: bf16 x bf16 -> fp32, M = 128.
-__host__ __device__ constexpr uint32_t product(int N, bool b_transposed) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_transposed ? 1u << 16 : 0u) | (uint32_t(N / 8) << 17) |
-         (uint32_t(kStreamRows / 16) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
-      : "memory");
-}
 
 // ---------------------------------------------------------------- the kernel
 
@@ -340,7 +259,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t at = (k / 4) * S::kSlabBytes + (k % 4) * 32;
-          mma_ss(tmem + st * 128, operand(qa + at, 16, 1024), operand(ka + at, 16, 1024), product(kTileKeys, false),
+          mma_ss(tmem + st * 128, operand<64>(qa + at, 16), operand<64>(ka + at, 16),
+                 product(kTileKeys, false, false),
                  k > 0);
         }
         tc_commit(&bar_s[st]);
@@ -359,8 +279,8 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
         const uint32_t va = smem_addr(ring + slot * S::kSlotBytes);
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand(va + k * 2048, S::kSlabBytes, 1024),
-                 product(D, true), !first || k > 0);
+          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<64>(va + k * 2048, S::kSlabBytes),
+                 product(D, false, true), !first || k > 0);
         if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
         if (w + 2 < work) scores(w + 2);
       }

@@ -61,18 +61,24 @@ RowsKernel rows_kernel_of(int D, int style) {
 
 struct AttendKernel {
   void (*fn)(isq::AttendArgs, CUtensorMap, CUtensorMap);
-  int smem, threads, keys;  // keys of a tile
+  int smem, threads, rows;  // rows of a unit
 };
-template <int D>
+// The streaming kernel for units of 16, 32 or 64 rows (head_dim 256: 16).
+template <int D, int NR>
 AttendKernel attend_rows_of() {
-  return {&isq::attend_rows_kernel<D>, isq::RowsShape<D>::kSmemBytes, isq::RowsShape<D>::kWarps * 32, isq::RowsShape<D>::kKeys};
+  return {&isq::attend_rows_kernel<D, NR>, isq::RowsShape<D, NR>::kSmemBytes, isq::kRowsThreads, NR};
 }
-AttendKernel attend_rows_of(int D) {
+template <int D>
+AttendKernel attend_rows_of(int64_t most) {
+  return most <= 16 ? attend_rows_of<D, 16>() : most <= 32 ? attend_rows_of<D, 32>() : attend_rows_of<D, 64>();
+}
+// For requests of up to `most` rows per KV head.
+AttendKernel attend_rows_of(int D, int64_t most) {
   switch (D) {
-    case 32: return attend_rows_of<32>();
-    case 64: return attend_rows_of<64>();
-    case 128: return attend_rows_of<128>();
-    default: return attend_rows_of<256>();
+    case 32: return attend_rows_of<32>(most);
+    case 64: return attend_rows_of<64>(most);
+    case 128: return attend_rows_of<128>(most);
+    default: return attend_rows_of<256, 16>();
   }
 }
 
@@ -80,7 +86,7 @@ AttendKernel attend_rows_of(int D) {
 template <int D>
 AttendKernel attend_tiles_of(bool shared) {
   return {shared ? &isq::attend_tiles_kernel<D, true> : &isq::attend_tiles_kernel<D, false>,
-          isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads, isq::kTileKeys};
+          isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads, isq::kUnitRows};
 }
 AttendKernel attend_tiles_of(int D, bool shared) {
   if (D == 64) return attend_tiles_of<64>(shared);
@@ -88,8 +94,8 @@ AttendKernel attend_tiles_of(int D, bool shared) {
   return {nullptr, 0, 0, 0};
 }
 
-// Rows of a KV head and request up to which the keys are streamed past 16-row
-// tiles (attend_rows) instead of 128-row ones (attend_tiles).
+// Rows of a KV head and request up to which attend_rows takes them, if
+// attend_tiles could.
 constexpr int kMostNarrowRows = 64;
 // Splits of a unit's keys in a cluster, and the keys that a split should at
 // least have.
@@ -103,6 +109,7 @@ constexpr int kMostParts = 16;
 // What an attention call launches; all from the host's numbers.
 struct AttendPlan {
   bool wide;             // attend_tiles over requests, else attend_rows
+  AttendKernel kernel;
   int64_t units;         // of the requests' grid
   int32_t splits;        // its splits (attend_rows: a cluster)
   int32_t parts;         // splits of the shared prefix's grid; 0: no such grid
@@ -119,7 +126,8 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   const int64_t most = int64_t(std::min(a->max_q_len, a->num_tokens)) * group;
   const bool has_tiles = attend_tiles_of(q->head_dim, false).fn != nullptr;
   p.wide = has_tiles && most > kMostNarrowRows;
-  const int64_t unit_rows = p.wide ? isq::kUnitRows : isq::kTileRows;
+  p.kernel = p.wide ? attend_tiles_of(q->head_dim, false) : attend_rows_of(q->head_dim, most);
+  const int64_t unit_rows = p.kernel.rows;
   // one unit per request where it holds all the request's rows, else at most
   // a partial unit per request more than the rows fill
   p.units = most <= unit_rows ? a->num_requests : (rows + unit_rows - 1) / unit_rows + a->num_requests;
@@ -161,15 +169,15 @@ uint16_t* layer_of(void* cache, const is_cache_t* c, int32_t layer) {
   return static_cast<uint16_t*>(cache) + int64_t(layer) * c->layer_stride;
 }
 
-// Tensor maps of a layer's K and V for a kernel's tiles: [D][B][blocks][heads]
-// with the cache's strides, in boxes of 64 dims (32 for D = 32) x the largest
-// power of two of tokens that divides the block and the tile.  Returns that
-// power's logarithm, or -1 where no box of 8 tokens fits or the cache's
-// strides have no map (the kernels then gather key by key).
-int box_maps(const is_query* q, const isq::AttendArgs& a, int tile_keys, CUtensorMap& k, CUtensorMap& v) {
+// Tensor maps of a layer's K and V: [D][B][blocks][heads] with the cache's
+// strides, in boxes of 64 dims (32 for D = 32) x the largest power of two of
+// tokens that divides the block and a tile of keys.  Returns that power's
+// logarithm, or -1 where no box of 8 tokens fits or the cache's strides have
+// no map (the kernels then gather key by key).
+int box_maps(const is_query* q, const isq::AttendArgs& a, CUtensorMap& k, CUtensorMap& v) {
   int box = 0;
-  while ((2 << box) <= tile_keys && a.block_size % (2 << box) == 0) ++box;
-  if (box < 3 || !q->encode) return -1;
+  while ((2 << box) <= isq::kTileKeys && a.block_size % (2 << box) == 0) ++box;
+  if (box < 3) return -1;
   const int D = q->head_dim, slab = std::min(D, 64);
   const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(a.block_size), cuuint64_t(a.num_blocks), cuuint64_t(a.kv_heads)};
   const cuuint64_t strides[3] = {cuuint64_t(a.token_stride) * 2, cuuint64_t(a.block_stride) * 2,
@@ -250,16 +258,13 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
   // Attributes now, so that the calls are launches alone (the functions are
   // loaded here, not inside somebody's stream capture).
   cudaFuncAttributes attr;
-  const AttendKernel ar = attend_rows_of(c.head_dim);
   bool ok = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(rows_kernel_of(c.head_dim, c.rope_style))) ==
-                cudaSuccess &&
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(ar.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 ar.smem) == cudaSuccess;
-  for (bool shared : {false, true}) {
-    const AttendKernel at = attend_tiles_of(c.head_dim, shared);
-    ok = ok && (!at.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(at.fn),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, at.smem) == cudaSuccess);
-  }
+            cudaSuccess;
+  for (const AttendKernel& k : {attend_rows_of(c.head_dim, 16), attend_rows_of(c.head_dim, 32),
+                                attend_rows_of(c.head_dim, 64), attend_tiles_of(c.head_dim, false),
+                                attend_tiles_of(c.head_dim, true)})
+    ok = ok && (!k.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) == cudaSuccess);
   void* encode = nullptr;
   cudaDriverEntryPointQueryResult found{};
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &encode, 12000, cudaEnableDefault, &found) ==
@@ -421,6 +426,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   a.st = query->status;
 
   CUtensorMap k_map{}, v_map{};
+  a.box_log2 = box_maps(query, a, k_map, v_map);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -431,7 +437,6 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
     sa.part_ml = a.part_ml = static_cast<float2*>(workspace);
     sa.part_o = a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
     const AttendKernel k = attend_tiles_of(query->head_dim, true);
-    sa.box_log2 = box_maps(query, sa, k.keys, k_map, v_map);
     cfg.gridDim = dim3(unsigned(shared_grid));
     cfg.blockDim = dim3(unsigned(k.threads));
     cfg.dynamicSmemBytes = size_t(k.smem);
@@ -451,8 +456,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.splits), 1, 1};
   }
-  const AttendKernel k = p.wide ? attend_tiles_of(query->head_dim, false) : attend_rows_of(query->head_dim);
-  a.box_log2 = box_maps(query, a, k.keys, k_map, v_map);
+  const AttendKernel& k = p.kernel;
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(k.threads));
   cfg.dynamicSmemBytes = size_t(k.smem);
