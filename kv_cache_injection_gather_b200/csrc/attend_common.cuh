@@ -32,6 +32,7 @@ struct AttendArgs {
   // Keys of one tensor-map box (a power of two that divides the block size and
   // the kernel's tile), as a logarithm; -1: gather by rows.
   int32_t box_log2;
+  int32_t head_slabs;          // slabs of dims between the maps' KV heads
   float scale_log2;            // scale * log2(e)
   int32_t num_heads;           // query heads
   int32_t group;               // query heads per KV head
@@ -95,18 +96,26 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
+// True in one lane of a converged warp.  The compiler knows it for one lane, so
+// copies and products issued under it need no loop over lanes for their
+// uniform operands (a lane-by-lane issue took 85 cycles an instruction).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // One arrival that also announces bytes.
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
-// A box of the paged cache to shared memory: dims from `x`, tokens from `token`
-// of block `block`, KV head h.  x is a multiple of 64 (or 0).
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t token, int32_t block,
-                                         int32_t h, uint64_t* bar) {
+// A box of the paged cache to shared memory: all dims of one head (`slab`: its
+// first slab's number), tokens from 8 * group of `block`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int32_t slab, int32_t group,
+                                         int32_t block, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(dst),
-      "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(token), "r"(block), "r"(h)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %4, %5, "
+      "%6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_addr(bar)), "r"(0), "r"(slab), "r"(group), "r"(block)
       : "memory");
 }
 __device__ __forceinline__ void fetch_map(const CUtensorMap* map) {
@@ -202,15 +211,13 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand descriptor (version 1) of a tile_at layout: 128-byte
-// swizzle for rows of 64 dims (layout 2), 64-byte for rows of 32 (layout 4).
-// lead: bytes between a transposed operand's slabs; the other stride, between
-// groups of 8 rows, follows from the row's width.
-template <int SLAB_DIMS>
+// Shared-memory operand descriptor (version 1) of a tile_at<D> layout: 128-byte
+// swizzle for slabs of 64 dims (layout 2), 64-byte for one of 32 (layout 4).
+// lead: bytes between the slabs of a transposed operand.
+template <int D>
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  static_assert(SLAB_DIMS == 64 || SLAB_DIMS == 32, "two swizzles");
-  return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(lead >> 4) << 16) | (uint64_t(SLAB_DIMS * 16 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(SLAB_DIMS == 64 ? 2 : 4) << 61);
+  return uint64_t((addr & 0x3ffff) >> 4) | (uint64_t(lead >> 4) << 16) | (uint64_t(D * 16 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(D < 64 ? 4 : 2) << 61);
 }
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128.  An operand that is
 // stored with its product dimension (keys) across rows is transposed.
@@ -372,9 +379,9 @@ __device__ __forceinline__ void check_requests(const AttendArgs& a) {
 
 // Table entry of position j (below the request's limit): the shared list's
 // below table_shared, the request's own otherwise.
-__device__ __forceinline__ int32_t table_entry(const AttendArgs& a, int32_t r, int32_t j) {
+__device__ __forceinline__ const int32_t* table_slot(const AttendArgs& a, int32_t r, int32_t j) {
   const int32_t jb = j / a.block_size;
-  return j < a.table_shared ? a.shared_blocks[jb] : a.block_tables[int64_t(r) * a.max_blocks + jb];
+  return j < a.table_shared ? a.shared_blocks + jb : a.block_tables + int64_t(r) * a.max_blocks + jb;
 }
 // Element offset of (position j in block `entry`, KV head h) in the layer's
 // caches; -1 for a block outside the cache, which is recorded.
@@ -386,22 +393,143 @@ __device__ __forceinline__ int64_t entry_offset(const AttendArgs& a, int32_t r, 
   return entry * a.block_stride + int64_t(j % a.block_size) * a.token_stride + h * a.head_stride;
 }
 __device__ __forceinline__ int64_t key_offset(const AttendArgs& a, int32_t r, int32_t h, int32_t j) {
-  return entry_offset(a, r, h, j, table_entry(a, r, j));
+  return entry_offset(a, r, h, j, *table_slot(a, r, j));
 }
 
 // ---------------------------------------------------------------- tiles
 
 constexpr int kTileKeys = 128;
-constexpr int kBoxDims = 64;   // dims of a slab (32 for D = 32)
 
-// Byte offset of 16-byte chunk c of row `row` in a tile of `keys` rows: the
-// chunks of a slab's row are permuted by the row's number (the 128-byte
-// swizzle; the 64-byte one for D = 32), so that 8 consecutive rows at one
-// chunk, an ldmatrix phase, fall into different banks.
+// A tile of bf16 rows of D values: groups of 8 rows, in them slabs of 64 dims
+// (one of 32 for D = 32), in them the rows, their 16-byte chunks permuted by
+// the row's number (the 128- and the 64-byte swizzle).  It is what the tensor
+// cores read in both directions and what a tensor-map box of 8 tokens x slabs
+// x groups of 8 writes in one go.  Byte offset of chunk c of a row:
 template <int D>
-__device__ __forceinline__ uint32_t tile_at(int keys, int row, int c) {
+__device__ __forceinline__ uint32_t tile_at(int row, int c) {
   if constexpr (D < 64) return uint32_t(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-  return uint32_t((c >> 3) * keys * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+  return uint32_t((row >> 3) * (D * 16) + (c >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+constexpr int kSlabStep = 1024;  // bytes between the slabs of a group (D >= 64)
+// Byte offset of 16 dims at 16 * k, for all rows (the start of a product's
+// step along the dims).
+template <int D>
+__device__ __forceinline__ uint32_t dims_at(int k) {
+  return uint32_t((k >> 2) * kSlabStep + (k & 3) * 32);
+}
+
+constexpr int kGatherWarps = 4;
+
+// Warp g of kGatherWarps brings the tiles K0 V0 K1 V1 ... of keys [lo, hi) of
+// request r and KV head h into a ring of NS slots of kTileKeys x D.  full[]
+// take kGatherWarps arrivals, empty[] one (a product's commit).  A tile comes as
+// boxes, or key by key (keys outside [first_key, hi) as zeros) where a box
+// holds keys of two blocks and where there is no map; with ZERO_EDGE also
+// values that run past hi.  Boxes leave keys outside the range as they find
+// them.  A block outside the cache sets *bad, and its keys mean nothing.
+template <int D, int NS, bool ZERO_EDGE>
+__device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map,
+                                             int g, int32_t r, int32_t h, int32_t lo, int32_t hi, int32_t tiles,
+                                             unsigned char* ring, uint64_t* full, uint64_t* empty,
+                                             volatile int32_t* failed, int32_t* bad) {
+  constexpr int CPR = D / 8, kSlotBytes = kTileKeys * D * 2, kMostBoxes = kTileKeys / 8 / kGatherWarps;
+  const int lane = threadIdx.x & 31;
+  const int32_t bits = max(0, a.box_log2);
+  const int32_t slab = h * a.head_slabs;
+  auto by_box = [&](int32_t j0, bool v) {
+    const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys && (a.table_shared & ((1 << bits) - 1)) != 0;
+    return a.box_log2 >= 0 && !torn && !(ZERO_EDGE && v && hi - j0 < kTileKeys);
+  };
+  // This warp's boxes are g, g + kGatherWarps, ...; lane i looks up the i-th of
+  // them, a tile ahead of the copies that need it.
+  const int32_t my_key = (lane * kGatherWarps + g) << bits;
+  auto position = [&](int32_t t) -> int32_t {
+    const int32_t j0 = lo + t * kTileKeys;
+    return a.box_log2 >= 0 && t < tiles && lane < kMostBoxes && my_key < kTileKeys && hi - j0 > my_key ? j0 + my_key : -1;
+  };
+  // (a load in every case: one under a condition would be waited for there)
+  auto look_up = [&](int32_t pos) -> int32_t { return *(pos < 0 ? a.q_offsets : table_slot(a, r, pos)); };
+  int32_t next_pos = position(0), next_entry = look_up(next_pos);
+  int32_t block[kMostBoxes], group[kMostBoxes];
+  uint32_t good = 0;
+  if (g == 0 && lane == 0) {
+    fetch_map(k_map);
+    fetch_map(v_map);
+  }
+  int32_t u = 0;
+  for (; u < 2 * tiles; ++u) {
+    const int slot = u % NS;
+    const bool v = u & 1;
+    const int32_t j0 = lo + (u >> 1) * kTileKeys;
+    if (!v) {
+      const int32_t pos = next_pos, entry = next_entry;
+      const bool fine = entry >= 0 && entry < a.num_blocks;
+      good = __ballot_sync(0xffffffffu, pos >= 0 && fine);
+      if (pos >= 0 && !fine && by_box(j0, false)) {
+        record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
+        *bad = 1;
+      }
+      const int32_t in_block = pos < 0 ? 0 : (pos % a.block_size) >> 3;
+#pragma unroll
+      for (int i = 0; i < kMostBoxes; ++i) {
+        block[i] = __shfl_sync(0xffffffffu, entry, i);
+        group[i] = __shfl_sync(0xffffffffu, in_block, i);
+      }
+      next_pos = position((u >> 1) + 1);
+      next_entry = look_up(next_pos);
+    }
+    // the whole warp goes on or stops
+    if (u >= NS && !__all_sync(0xffffffffu, bar_wait(&empty[slot], ((u / NS) - 1) & 1, failed))) break;
+    const uint32_t dst = smem_addr(ring + slot * kSlotBytes);
+    if (by_box(j0, v)) {
+      const CUtensorMap* map = v ? v_map : k_map;
+      if (elect_one()) {
+        bar_expect(&full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
+#pragma unroll
+        for (int i = 0; i < kMostBoxes; ++i)
+          if ((good >> i) & 1u)
+            copy_box(dst + ((i * kGatherWarps + g) << bits) * (D * 2), map, slab, group[i], block[i], &full[slot]);
+      }
+    } else {
+      const uint16_t* cache = v ? a.v_cache : a.k_cache;
+      for (int first = 32 * g; first < kTileKeys; first += 32 * kGatherWarps) {
+        const int32_t j = j0 + first + lane;
+        int64_t at = -1;
+        if (hi - j0 > first + lane && j >= a.first_key) {
+          at = key_offset(a, r, h, j);
+          if (at < 0) *bad = 1;
+        }
+#pragma unroll 4
+        for (int n = 0; n < CPR; ++n) {
+          const int e = n * 32 + lane, row = e / CPR, c = e % CPR;
+          const int64_t from = __shfl_sync(0xffffffffu, at, row);
+          cp_async16(dst + tile_at<D>(first + row, c), cache + (from < 0 ? 0 : from + c * 8), from < 0 ? 0 : 16);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&full[slot]);
+    }
+  }
+  if (*failed)  // copies in flight: nothing may leave before they land
+    for (int32_t i = max(0, u - NS); i < u; ++i) bar_wait(&full[i % NS], (i / NS) & 1, nullptr);
+}
+
+// Queries of `rows` rows to a tile, zeros up to `count`, by `threads` threads.
+template <int D, typename Source>
+__device__ __forceinline__ void load_queries(unsigned char* tile, int rows, int count, int thread, int threads,
+                                             const uint16_t* any, Source source) {
+  constexpr int CPR = D / 8;
+  for (int i = thread; i < count * CPR; i += threads) {
+    const int row = i / CPR, c = i % CPR;
+    const bool live = row < rows;
+    cp_async16(smem_addr(tile + tile_at<D>(row, c)), live ? source(row) + c * 8 : any, live ? 16 : 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  proxy_fence();
 }
 
 // One row over keys [lo, hi) by a warp, key after key in fp32: for rows whose

@@ -28,14 +28,12 @@
 
 namespace isq {
 
-constexpr int kRowsThreads = 6 * 32;
+constexpr int kRowsThreads = (4 + kGatherWarps + 1) * 32;
+constexpr int kProductWarp = 4 + kGatherWarps;
 
 template <int D, int NR>
 struct RowsShape {
-  static constexpr int kSlabDims = D < 64 ? D : 64;
-  static constexpr int kSlabs = D / kSlabDims;
-  static constexpr int kSlabBytes = kTileKeys * kSlabDims * 2;
-  static constexpr int kSlotBytes = kSlabs * kSlabBytes;       // one K or V tile
+  static constexpr int kSlotBytes = kTileKeys * D * 2;         // one K or V tile
   static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR > 32 ? 5 : 6) : D == 64 ? 10 : 16;
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kPBytes = NR * kTileKeys * 2;           // twice
@@ -53,10 +51,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
     const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using S = RowsShape<D, NR>;
-  constexpr int CPR = D / 8, NS = S::kSlots, SL = S::kSlabs;
+  constexpr int CPR = D / 8, NS = S::kSlots;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o, bar_end;
-  __shared__ float s_top[4][NR], s_m[NR], s_l[NR];
+  __shared__ __align__(16) float s_m[NR];
+  __shared__ float s_top[4][NR], s_l[NR];
   __shared__ int32_t s_lim[NR], s_odd[NR];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], 32);
+      bar_init(&bar_full[i], kGatherWarps);
       bar_init(&bar_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -115,96 +114,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
   }
   if (tid < NR) {
     s_lim[tid] = tid < rows ? min(hi, row_limit(a, rq, token_of(tid))) : hi;
-    s_m[tid] = neg_inf();
+    // rows that are not there never rise above their reference
+    s_m[tid] = tid < rows ? neg_inf() : -neg_inf();
     s_l[tid] = 0.f;
     s_odd[tid] = 0;
   }
-  if (warp == 5) tmem_alloc(&s_tmem, S::kColumns);
+  if (warp == kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;               // S^T, twice NR columns
   const uint32_t tmem_o = tmem + 2 * NR;      // O^T, NR columns per 128 dims
 
-  if (warp == 4) {
-    // ---------------- gather: tiles K0 V0 K1 V1 ...
-    if (lane == 0) {
-      fetch_map(&k_map);
-      fetch_map(&v_map);
-    }
-    // A tile comes as boxes, or key by key where a box holds keys of two
-    // blocks and where there is no map.
-    const int32_t bits = max(0, a.box_log2), boxes = kTileKeys >> bits;
-    auto by_box = [&](int32_t j0) {
-      const bool torn =
-          j0 < a.table_shared && a.table_shared - j0 < kTileKeys && (a.table_shared & ((1 << bits) - 1)) != 0;
-      return a.box_log2 >= 0 && !torn;
-    };
-    // lane i looks up box i of a tile, a tile ahead of the copies that need it
-    auto position = [&](int32_t t) -> int32_t {
-      const int32_t j0 = lo + t * kTileKeys;
-      return a.box_log2 >= 0 && t < tiles && lane < boxes && hi - j0 > lane << bits ? j0 + (lane << bits) : -1;
-    };
-    int32_t next_pos = position(0), next_entry = next_pos < 0 ? -1 : table_entry(a, r, next_pos);
-    int32_t pos = -1, entry = -1;
-    uint32_t good = 0;
-    int32_t u = 0;
-    for (; u < 2 * tiles; ++u) {
-      const int slot = u % NS;
-      const bool v = u & 1;
-      const int32_t j0 = lo + (u >> 1) * kTileKeys;
-      if (!v) {
-        pos = next_pos;
-        entry = next_entry;
-        next_pos = position((u >> 1) + 1);
-        if (next_pos >= 0) next_entry = table_entry(a, r, next_pos);
-        good = __ballot_sync(0xffffffffu, pos >= 0 && entry >= 0 && entry < a.num_blocks);
-        if (by_box(j0) && pos >= 0 && !((good >> lane) & 1u)) {
-          record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
-          s_bad = 1;
-        }
-      }
-      // the whole warp goes on or stops
-      if (u >= NS && !__all_sync(0xffffffffu, bar_wait(&bar_empty[slot], ((u / NS) - 1) & 1, &s_failed))) break;
-      const uint32_t dst = smem_addr(ring + slot * S::kSlotBytes);
-      if (by_box(j0)) {
-        if (lane == 0) bar_expect(&bar_full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
-        else bar_arrive(&bar_full[slot]);
-        for (int first = 0; first < boxes * SL; first += 32) {
-          const int op = first + lane, box = op / SL, slab = op % SL;
-          const int32_t b = __shfl_sync(0xffffffffu, entry, box & 31), at = __shfl_sync(0xffffffffu, pos, box & 31);
-          if (op < boxes * SL && ((good >> box) & 1u))
-            copy_box(dst + slab * S::kSlabBytes + (box << bits) * (S::kSlabDims * 2), v ? &v_map : &k_map,
-                     slab * S::kSlabDims, at % a.block_size, b, h, &bar_full[slot]);
-        }
-      } else {
-        const uint16_t* cache = v ? a.v_cache : a.k_cache;
-        for (int first = 0; first < kTileKeys; first += 32) {
-          const int32_t j = j0 + first + lane;
-          int64_t at = -1;
-          if (hi - j0 > first + lane && j >= a.first_key) {
-            at = key_offset(a, r, h, j);
-            if (at < 0) s_bad = 1;
-          }
-#pragma unroll 4
-          for (int n = 0; n < CPR; ++n) {
-            const int e = n * 32 + lane, row = e / CPR, c = e % CPR;
-            const int64_t from = __shfl_sync(0xffffffffu, at, row);
-            cp_async16(dst + tile_at<D>(kTileKeys, first + row, c), cache + (from < 0 ? 0 : from + c * 8),
-                       from < 0 ? 0 : 16);
-          }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        proxy_fence();
-        bar_arrive(&bar_full[slot]);
-      }
-    }
-    if (*static_cast<volatile int32_t*>(&s_failed))  // copies in flight: nothing may leave before they land
-      for (int32_t i = max(0, u - NS); i < u; ++i) bar_wait(&bar_full[i % NS], (i / NS) & 1, nullptr);
-  } else if (warp == 5) {
+  if (warp >= 4 && warp < kProductWarp) {
+    gather_tiles<D, NS, false>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
+                               &s_bad);
+  } else if (warp == kProductWarp) {
     // ---------------- products
-    if (lane == 0 && tiles > 0) {
+    if (tiles > 0 && elect_one()) {
       bool ok = bar_wait(&bar_q, 0, &s_failed);
       auto wait_tile = [&](int32_t u) { ok = ok && bar_wait(&bar_full[u % NS], (u / NS) & 1, &s_failed); };
       auto scores = [&](int32_t t) {
@@ -214,11 +141,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
         tc_fence_after();
         const uint32_t ka = smem_addr(ring + slot * S::kSlotBytes), qa = smem_addr(q_tile);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int slab = k * 16 / S::kSlabDims, in = (k * 16 % S::kSlabDims) * 2;
-          mma_ss(tmem + (t & 1) * NR, operand<S::kSlabDims>(ka + slab * S::kSlabBytes + in, 16),
-                 operand<S::kSlabDims>(qa + slab * (NR * S::kSlabDims * 2) + in, 16), product(NR, false, false), k > 0);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + (t & 1) * NR, operand<D>(ka + dims_at<D>(k), 16), operand<D>(qa + dims_at<D>(k), 16),
+                 product(NR, false, false), k > 0);
         tc_commit(&bar_s[t & 1]);
         tc_commit(&bar_empty[slot]);
       };
@@ -237,11 +162,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
 #pragma unroll
           for (int k = 0; k < kTileKeys / 16; ++k)
             // V^T: 128 rows of dims; with D below 128 its slabs repeat (lead 0)
-            mma_ss(tmem_o + g * NR,
-                   operand<S::kSlabDims>(va + g * 2 * S::kSlabBytes + k * 16 * (S::kSlabDims * 2),
-                                         D < 128 ? 0 : S::kSlabBytes),
-                   operand<64>(pa + (k / 4) * (NR * 128) + (k % 4) * 32, 16), product(NR, true, false),
-                   t > 0 || k > 0);
+            mma_ss(tmem_o + g * NR, operand<D>(va + g * 2 * kSlabStep + k * (D * 32), D < 128 ? 0 : kSlabStep),
+                   operand<128>(pa + dims_at<128>(k), 16), product(NR, true, false), t > 0 || k > 0);
         tc_commit(&bar_empty[slot]);
         tc_commit(&bar_o);
       }
@@ -253,16 +175,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
     __syncwarp();
   } else {
     // ---------------- softmax, one key a thread
-    for (int i = tid; i < NR * CPR; i += 128) {
-      const int row = i / CPR, c = i % CPR;
-      const bool live = row < rows;
-      const uint16_t* src = a.q.data;
-      if (live) src += int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs + c * 8;
-      cp_async16(smem_addr(q_tile + tile_at<D>(NR, row, c)), src, live ? 16 : 0);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    proxy_fence();
+    load_queries<D>(q_tile, rows, NR, tid, 128, a.q.data, [&](int row) {
+      return a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs;
+    });
     bar_arrive(&bar_q);
 
     const int32_t lim_min = s_lim[0];  // limits rise with the rows
@@ -285,7 +200,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
         if (ok && !in) {
           unsigned char* row = ring + (u % NS) * S::kSlotBytes;
           for (int c = 0; c < CPR; ++c)
-            *reinterpret_cast<uint4*>(row + tile_at<D>(kTileKeys, tid, c)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(row + tile_at<D>(tid, c)) = make_uint4(0, 0, 0, 0);
         }
       }
       ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_s[t & 1], (t >> 1) & 1, &s_failed));
@@ -298,14 +213,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
       const bool masked = edge || j0 + kTileKeys > lim_min;
       float x[NR];
       bool above = false;
+      // The reference m of a row follows its maximum only when that has risen
+      // by more than 2^8: smaller steps leave P below 2^8 and the sums as they
+      // are.  (-inf + 8 is -inf: the first seen key counts.)
 #pragma unroll
-      for (int c = 0; c < NR; ++c) {
-        x[c] = ok ? __uint_as_float(v[c]) * a.scale_log2 : neg_inf();
-        if (masked && (!in || j >= s_lim[c])) x[c] = neg_inf();
-        // The reference m of a row follows its maximum only when that has
-        // risen by more than 2^8: smaller steps leave P below 2^8 and the
-        // sums as they are.  (-inf + 8 is -inf: the first seen key counts.)
-        if (c < rows) above = above || x[c] > s_m[c] + 8.f;
+      for (int c = 0; c < NR; c += 4) {
+        if (c >= rows) break;
+        const float4 m4 = *reinterpret_cast<const float4*>(&s_m[c]);
+        const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[c + i] = ok ? __uint_as_float(v[c + i]) * a.scale_log2 : neg_inf();
+          if (masked && (!in || j >= s_lim[c + i])) x[c + i] = neg_inf();
+          above = above || x[c + i] > m[i] + 8.f;
+        }
       }
       uint32_t any;
       asm volatile(
@@ -353,19 +274,22 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
         if (tid < rows) s_m[tid] = mine;
         asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
       }
-      // P^T as the second product's B operand: [row][128 keys], slabs of 64.
+      // P^T as the second product's B operand: a tile of [row][128 keys].
       // The probabilities are rounded to bf16: V, the other operand, is no
       // finer, and the sum l keeps them in fp32.
-      unsigned char* p = p_tiles + (t & 1) * S::kPBytes + (tid / 64) * (NR * 128) + (tid & 7) * 2;
-      const int chunk = (tid & 63) >> 3;
+      unsigned char* p = p_tiles + (t & 1) * S::kPBytes + (tid & 7) * 2;
 #pragma unroll
-      for (int c = 0; c < NR; ++c) {
+      for (int c = 0; c < NR; c += 4) {
         if (c >= rows) break;  // the products of other rows are not looked at
-        const float m = s_m[c];
-        const float e = exp2_fast(x[c] - (m == neg_inf() ? 0.f : m));  // no key seen yet: every term is 0
-        l[c] += e;
-        *reinterpret_cast<uint16_t*>(p + c * 128 + ((chunk ^ (c & 7)) << 4)) =
-            __bfloat16_as_ushort(__float2bfloat16_rn(e));
+        const float4 m4 = *reinterpret_cast<const float4*>(&s_m[c]);
+        const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = exp2_fast(x[c + i] - (m[i] == neg_inf() ? 0.f : m[i]));  // no key seen yet: every term is 0
+          l[c + i] += e;
+          *reinterpret_cast<uint16_t*>(p + tile_at<128>(c + i, tid >> 3)) =
+              __bfloat16_as_ushort(__float2bfloat16_rn(e));
+        }
       }
       proxy_fence();
       tc_fence_before();
@@ -410,7 +334,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, S::kColumns);
   }

@@ -29,15 +29,13 @@ namespace isq {
 
 constexpr int kStreamRows = 128;
 constexpr int kUnitRows = 2 * kStreamRows;
-constexpr int kTilesThreads = 13 * 32;
-constexpr int kLoadThreads = 128;
+constexpr int kTilesThreads = (8 + kGatherWarps + 1) * 32;
 
 template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kQBytes = kUnitRows * D * 2;
-  static constexpr int kSlabBytes = kTileKeys * 128;     // 64 dims of 128 rows
   // data, and up to 1 KB to align it
   static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
 };
@@ -71,7 +69,6 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
   constexpr int CPR = D / 8, NS = S::kSlots;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o;
-  __shared__ int64_t s_at[kTileKeys];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -123,14 +120,14 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], kLoadThreads);
+      bar_init(&bar_full[i], kGatherWarps);
       bar_init(&bar_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&bar_s[i], 1);
       bar_init(&bar_p[i], kStreamRows);
     }
-    bar_init(&bar_q, kLoadThreads);
+    bar_init(&bar_q, 2 * kStreamRows);
     bar_init(&bar_o, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_failed = 0;
@@ -148,104 +145,11 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
   int32_t lim = 0;
 
   if (warp >= 8 && warp < 12) {
-    // ---------------- gather: Q, then tiles K0 V0 K1 V1 ...
-    const int x = tid - 8 * 32;
-    const uint32_t q_dst = smem_addr(smem);
-    for (int e = x; e < (by_rows ? kUnitRows : kStreamRows) * CPR; e += kLoadThreads) {
-      const int row = e / CPR, c = e % CPR;
-      const bool live = row < rows;
-      const uint16_t* src = a.q.data;
-      if (live) src += int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs + c * 8;
-      const int st = row / kStreamRows, rr = row % kStreamRows;
-      cp_async16(q_dst + st * S::kSlotBytes + tile_at<D>(kStreamRows, rr, c), src, live ? 16 : 0);
-    }
-    cp_async_commit();
-    auto q_landed = [&] {
-      cp_async_wait<0>();
-      proxy_fence();
-      bar_arrive(&bar_q);
-    };
-    if (x == 0) {
-      fetch_map(&k_map);
-      fetch_map(&v_map);
-    }
-    // A tile comes as boxes (op = lane of the first warp: box lane / SL, slab
-    // lane % SL), or key by key: where a box holds keys of two blocks, where
-    // there is no map, and for values that run past hi, whose rows from there
-    // on have to be zeros.
-    constexpr int SL = D / 64;
-    const int32_t box_bits = max(0, a.box_log2), my_box = lane / SL << box_bits;
-    auto by_box = [&](int32_t j0, bool v) {
-      const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys &&
-                        (a.table_shared & ((1 << box_bits) - 1)) != 0;
-      return a.box_log2 >= 0 && !torn && !(v && hi - j0 < kTileKeys);
-    };
-    auto position = [&](int32_t t) -> int32_t {  // that this lane looks up for tile t as boxes
-      return t < tiles && my_box < kTileKeys && hi - (lo + t * kTileKeys) > my_box ? lo + t * kTileKeys + my_box : -1;
-    };
-    int32_t pos = -1, entry = 0, next_pos = position(0);
-    int32_t next_entry = next_pos < 0 || a.box_log2 < 0 ? 0 : table_entry(a, r, next_pos);
-    const int32_t total = 2 * tiles;
-    for (int32_t u = 0; u < total; ++u) {
-      const int slot = u % NS;
-      const bool v = u & 1;
-      const int32_t j0 = lo + (u >> 1) * kTileKeys;
-      if (!v) {
-        pos = next_pos;
-        entry = next_entry;
-        next_pos = position((u >> 1) + 1);  // read a tile ahead of the copies that need it
-        if (next_pos >= 0 && a.box_log2 >= 0) next_entry = table_entry(a, r, next_pos);
-      }
-      // after a wait that gave up the loop runs out without copies
-      const bool ok = u < NS || bar_wait(&bar_empty[slot], ((u / NS) - 1) & 1, &s_failed);
-      const uint32_t dst = smem_addr(ring + slot * S::kSlotBytes);
-      if (by_box(j0, v)) {
-        if (warp == 8) {
-          const bool good = ok && pos >= 0 && entry >= 0 && entry < a.num_blocks;
-          if (pos >= 0 && !(entry >= 0 && entry < a.num_blocks)) {
-            record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
-            s_bad = 1;
-          }
-          const uint32_t ops = __ballot_sync(0xffffffffu, good);
-          if (lane == 0) bar_expect(&bar_full[slot], (uint32_t(__popc(ops)) << box_bits) * 128);
-          else bar_arrive(&bar_full[slot]);
-          if (good)
-            copy_box(dst + lane % SL * S::kSlabBytes + my_box * 128, v ? &v_map : &k_map, lane % SL * 64,
-                     pos % a.block_size, entry, h, &bar_full[slot]);
-        } else {
-          bar_arrive(&bar_full[slot]);
-        }
-      } else {
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // s_at of the tile before is read
-        int64_t at = -1;
-        if (hi - j0 > x) {
-          at = key_offset(a, r, h, j0 + x);
-          if (at < 0) s_bad = 1;
-        }
-        s_at[x] = at;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const uint16_t* cache = v ? a.v_cache : a.k_cache;
-        if (ok) {
-#pragma unroll 4
-          for (int n = 0; n < kTileKeys * CPR / kLoadThreads; ++n) {
-            const int e = n * kLoadThreads + x, row = e / CPR, c = e % CPR;
-            const int64_t from = s_at[row];
-            cp_async16(dst + tile_at<D>(kTileKeys, row, c), cache + (from < 0 ? 0 : from + c * 8), from < 0 ? 0 : 16);
-          }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        proxy_fence();
-        bar_arrive(&bar_full[slot]);
-      }
-      if (u == min(total, NS) - 1) q_landed();  // the ring is full of copies by now
-    }
-    cp_async_wait<0>();
-    if (*static_cast<volatile int32_t*>(&s_failed))  // copies in flight: nothing may leave before they land
-      for (int32_t u = max(0, total - NS); u < total; ++u) bar_wait(&bar_full[u % NS], (u / NS) & 1, nullptr);
+    gather_tiles<D, NS, true>(a, &k_map, &v_map, warp - 8, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
+                              &s_bad);
   } else if (warp == 12) {
     // ---------------- products
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       auto tile_of = [&](int32_t w) { return by_rows ? w >> 1 : w; };
       auto wait_tile = [&](int32_t u) { ok = ok && bar_wait(&bar_full[u % NS], (u / NS) & 1, &s_failed); };
@@ -257,12 +161,9 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
         const uint32_t qa = smem_addr(smem) + (by_rows ? st * S::kSlotBytes : 0);
         const uint32_t ka = smem_addr(ring + slot * S::kSlotBytes);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k / 4) * S::kSlabBytes + (k % 4) * 32;
-          mma_ss(tmem + st * 128, operand<64>(qa + at, 16), operand<64>(ka + at, 16),
-                 product(kTileKeys, false, false),
-                 k > 0);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + st * 128, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
+                 product(kTileKeys, false, false), k > 0);
         tc_commit(&bar_s[st]);
         if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
       };
@@ -279,7 +180,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
         const uint32_t va = smem_addr(ring + slot * S::kSlotBytes);
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<64>(va + k * 2048, S::kSlabBytes),
+          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<D>(va + k * (D * 32), kSlabStep),
                  product(D, false, true), !first || k > 0);
         if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
         if (w + 2 < work) scores(w + 2);
@@ -290,6 +191,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
     __syncwarp();
   } else if (warp < 8) {
     // ---------------- softmax of stream st, one row a thread
+    load_queries<D>(smem, rows, by_rows ? kUnitRows : kStreamRows, tid, 2 * kStreamRows, a.q.data, [&](int row) {
+      return a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs;
+    });
+    bar_arrive(&bar_q);
     const int st = warp / 4, row = (tid & 127) + (by_rows ? st * kStreamRows : 0);
     lim = row < rows ? min(hi, limit_of(row)) : hi;
     const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);

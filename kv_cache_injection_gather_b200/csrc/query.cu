@@ -169,23 +169,28 @@ uint16_t* layer_of(void* cache, const is_cache_t* c, int32_t layer) {
   return static_cast<uint16_t*>(cache) + int64_t(layer) * c->layer_stride;
 }
 
-// Tensor maps of a layer's K and V: [D][B][blocks][heads] with the cache's
-// strides, in boxes of 64 dims (32 for D = 32) x the largest power of two of
-// tokens that divides the block and a tile of keys.  Returns that power's
-// logarithm, or -1 where no box of 8 tokens fits or the cache's strides have
-// no map (the kernels then gather key by key).
-int box_maps(const is_query* q, const isq::AttendArgs& a, CUtensorMap& k, CUtensorMap& v) {
+// Tensor maps of a layer's K and V with the cache's strides, as [64 dims]
+// [8 tokens][slabs of 64 dims][groups of 8 tokens][blocks] (32 dims for D =
+// 32); the head is a slab number.  A box is a head's dims x the largest power
+// of two of tokens that divides the block and a tile of keys.  Returns that
+// power's logarithm, or -1 where there is no such box: under 8 tokens, a head
+// stride between slabs, strides that a map cannot have (the kernels then
+// gather key by key).
+int box_maps(const is_query* q, isq::AttendArgs& a, CUtensorMap& k, CUtensorMap& v) {
   int box = 0;
   while ((2 << box) <= isq::kTileKeys && a.block_size % (2 << box) == 0) ++box;
-  if (box < 3) return -1;
   const int D = q->head_dim, slab = std::min(D, 64);
-  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(a.block_size), cuuint64_t(a.num_blocks), cuuint64_t(a.kv_heads)};
-  const cuuint64_t strides[3] = {cuuint64_t(a.token_stride) * 2, cuuint64_t(a.block_stride) * 2,
-                                 cuuint64_t(a.head_stride) * 2};
-  const cuuint32_t boxes[4] = {cuuint32_t(slab), cuuint32_t(1 << box), 1, 1}, ones[4] = {1, 1, 1, 1};
+  const int64_t slabs = (a.kv_heads - 1) * (a.head_stride / slab) + D / slab;
+  if (box < 3 || a.head_stride % slab != 0 || slabs > INT32_MAX) return -1;
+  a.head_slabs = int32_t(a.kv_heads > 1 ? a.head_stride / slab : 0);
+  const cuuint64_t dims[5] = {cuuint64_t(slab), 8, cuuint64_t(slabs), cuuint64_t(a.block_size / 8), cuuint64_t(a.num_blocks)};
+  const cuuint64_t strides[4] = {cuuint64_t(a.token_stride) * 2, cuuint64_t(slab) * 2, cuuint64_t(a.token_stride) * 16,
+                                 cuuint64_t(a.block_stride) * 2};
+  const cuuint32_t boxes[5] = {cuuint32_t(slab), 8, cuuint32_t(D / slab), cuuint32_t(1 << box) / 8, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   const CUtensorMapSwizzle swizzle = slab == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   for (int i = 0; i < 2; ++i)
-    if (q->encode(i ? &v : &k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(i ? a.v_cache : a.k_cache), dims,
+    if (q->encode(i ? &v : &k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint16_t*>(i ? a.v_cache : a.k_cache), dims,
                   strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return -1;
