@@ -240,6 +240,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
+// Largest of a warp's values (NaN left out).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- launches
 
 // Programmatic dependent launch: the next grid on the stream may start; wait

@@ -30,11 +30,15 @@ namespace isq {
 
 constexpr int kRowsThreads = (4 + kGatherWarps + 1) * 32;
 constexpr int kProductWarp = 4 + kGatherWarps;
+constexpr int kMostSplits = 8;  // CTAs of a cluster
 
 template <int D, int NR>
 struct RowsShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;         // one K or V tile
-  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR > 32 ? 5 : 6) : D == 64 ? 10 : 16;
+#ifndef V_S128
+#define V_S128 6
+#endif
+  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR > 32 ? 5 : NR > 16 ? 6 : V_S128) : D == 64 ? 10 : 16;
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kPBytes = NR * kTileKeys * 2;           // twice
   static constexpr int kRingBytes = kSlots * kSlotBytes;
@@ -47,7 +51,7 @@ struct RowsShape {
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
+__global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 == 3) ? 2 : 1) attend_rows_kernel(
     const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using S = RowsShape<D, NR>;
@@ -55,7 +59,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o, bar_end;
   __shared__ __align__(16) float s_m[NR];
-  __shared__ float s_top[4][NR], s_l[NR];
+  __shared__ __align__(16) float s_top[4][NR], s_shrink[NR];
+  __shared__ float s_l[NR], s_all_m[kMostSplits][NR], s_all_l[kMostSplits][NR];
   __shared__ int32_t s_lim[NR], s_odd[NR];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
@@ -71,10 +76,29 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
     wait_for_previous();
     return;
   }
+  // what needs no metadata first, beside the loads of find_unit
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(&bar_full[i], kGatherWarps);
+      bar_init(&bar_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bar_s[i], 1);
+      bar_init(&bar_p[i], 128);
+    }
+    bar_init(&bar_q, 128);
+    bar_init(&bar_o, 1);
+    bar_init(&bar_end, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_failed = 0;
+    s_bad = 0;
+  }
+  if (warp == kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   int32_t r, tile;
   Request rq;
   find_unit<NR, kRowsThreads>(a, cluster / a.kv_heads, r, tile, rq);
   if (r < 0) {  // so for the whole cluster
+    if (warp == kProductWarp) tmem_free(s_tmem, S::kColumns);
     wait_for_previous();  // on every path: the next grid relies on both
     return;
   }
@@ -96,30 +120,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
   unsigned char* p_tiles = ring + S::kRingBytes;
   unsigned char* q_tile = p_tiles + 2 * S::kPBytes;
 
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], kGatherWarps);
-      bar_init(&bar_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bar_s[i], 1);
-      bar_init(&bar_p[i], 128);
-    }
-    bar_init(&bar_q, 128);
-    bar_init(&bar_o, 1);
-    bar_init(&bar_end, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_failed = 0;
-    s_bad = 0;
-  }
   if (tid < NR) {
     s_lim[tid] = tid < rows ? min(hi, row_limit(a, rq, token_of(tid))) : hi;
     // rows that are not there never rise above their reference
     s_m[tid] = tid < rows ? neg_inf() : -neg_inf();
     s_l[tid] = 0.f;
+    s_shrink[tid] = 1.f;
     s_odd[tid] = 0;
   }
-  if (warp == kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -237,42 +245,45 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
           : "memory");
       if (any) {
 #pragma unroll
-        for (int c = 0; c < NR; ++c) {
+        for (int c = 0; c < NR; c += 4) {
           if (c >= rows) break;
-          float top = x[c];
+          float top[4];
 #pragma unroll
-          for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          if (lane == 0) s_top[warp][c] = top;
+          for (int i = 0; i < 4; ++i) top[i] = warp_max(x[c + i]);
+          if (lane == 0) *reinterpret_cast<float4*>(&s_top[warp][c]) = make_float4(top[0], top[1], top[2], top[3]);
         }
         asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-        auto top_of = [&](int c) {
-          return fmaxf(fmaxf(fmaxf(s_top[0][c], s_top[1][c]), fmaxf(s_top[2][c], s_top[3][c])), s_m[c]);
-        };
-        auto shrink_of = [&](int c) -> float {
-          const float top = top_of(c);
-          return top == neg_inf() ? 1.f : exp2_fast(s_m[c] - top);
-        };
-#pragma unroll
-        for (int c = 0; c < NR; ++c)
-          if (c < rows) l[c] *= shrink_of(c);
+        if (tid < rows) {
+          const float old = s_m[tid];
+          const float top = fmaxf(fmaxf(fmaxf(s_top[0][tid], s_top[1][tid]), fmaxf(s_top[2][tid], s_top[3][tid])), old);
+          s_m[tid] = top;
+          s_shrink[tid] = top == neg_inf() ? 1.f : exp2_fast(old - top);
+        }
+        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
         if (t > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_o, (t - 1) & 1, &s_failed));
         if (t > 0 && ok) {
           tc_fence_after();
+          constexpr int kPiece = NR < 32 ? NR : 32;  // columns at a time
 #pragma unroll
-          for (int g = 0; g < S::kGroups; ++g) {
-            tmem_ld<NR>(tmem_o + g * NR + lanes, v);
-            tmem_wait_ld();
+          for (int c0 = 0; c0 < NR; c0 += kPiece) {
+            float shrink[kPiece];
 #pragma unroll
-            for (int c = 0; c < NR; ++c)
-              if (c < rows) v[c] = __float_as_uint(__uint_as_float(v[c]) * shrink_of(c));
-            tmem_st<NR>(tmem_o + g * NR + lanes, v);
+            for (int c = 0; c < kPiece; c += 4) *reinterpret_cast<float4*>(&shrink[c]) =
+                *reinterpret_cast<const float4*>(&s_shrink[c0 + c]);
+#pragma unroll
+            for (int c = 0; c < kPiece; ++c) l[c0 + c] *= shrink[c];
+#pragma unroll
+            for (int g = 0; g < S::kGroups; ++g) {
+              uint32_t o[kPiece];
+              tmem_ld<kPiece>(tmem_o + g * NR + c0 + lanes, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < kPiece; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * shrink[c]);
+              tmem_st<kPiece>(tmem_o + g * NR + c0 + lanes, o);
+            }
           }
           tmem_wait_st();
         }
-        const float mine = tid < rows ? top_of(tid) : 0.f;
-        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");  // the old references are read
-        if (tid < rows) s_m[tid] = mine;
-        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
       }
       // P^T as the second product's B operand: a tile of [row][128 keys].
       // The probabilities are rounded to bf16: V, the other operand, is no
@@ -296,16 +307,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
       bar_arrive(&bar_p[t & 1]);
     }
     // ---- the CTA's sums
-    if (tiles > 0) bar_wait(&bar_o, (tiles - 1) & 1, &s_failed);
-    __syncwarp();
-    tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < NR; ++c) {
+    for (int c = 0; c < NR; c += 4) {
       if (c >= rows) break;
 #pragma unroll
-      for (int d = 16; d > 0; d /= 2) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-      if (lane == 0) s_top[warp][c] = l[c];
+      for (int d = 16; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[c + i] += __shfl_xor_sync(0xffffffffu, l[c + i], d);
+      if (lane == 0) *reinterpret_cast<float4*>(&s_top[warp][c]) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
     }
+    if (tiles > 0) bar_wait(&bar_o, (tiles - 1) & 1, &s_failed);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();  // every slot of the ring is free
@@ -359,26 +371,39 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attend_rows_kernel(
   wait_for_previous();
   const int64_t part_rows = int64_t(a.num_tokens) * a.num_heads;
   const uint32_t part_at = smem_addr(part), m_at = smem_addr(s_m), l_at = smem_addr(s_l);
+  for (int i = tid; i < rows * a.splits; i += kRowsThreads) {
+    const int row = i % rows, k = i / rows;
+    s_all_m[k][row] = ld_cluster(in_cta(m_at + row * 4, k));
+    s_all_l[k][row] = ld_cluster(in_cta(l_at + row * 4, k));
+  }
+  __syncthreads();
   for (int i = split * kRowsThreads + tid; i < rows * (D / 4); i += kRowsThreads * a.splits) {
     const int row = i / (D / 4), c = i % (D / 4);
     const int64_t t = rq.tok0 + token_of(row);
     const int32_t head = head_of(row);
     const int64_t part_row = t * a.num_heads + head;
+    float4 v[kMostSplits];
     float m = neg_inf();
-    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, ld_cluster(in_cta(m_at + row * 4, k)));
+#pragma unroll
+    for (int k = 0; k < kMostSplits; ++k)
+      if (k < a.splits) {
+        v[k] = ld_cluster4(in_cta(part_at + (row * D + c * 4) * 4, k));
+        m = fmaxf(m, s_all_m[k][row]);
+      }
     for (int k = 0; k < a.num_parts; ++k) m = fmaxf(m, __ldcg(&a.part_ml[k * part_rows + part_row].x));
     const float ref = m == neg_inf() ? 0.f : m;
     float l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < a.splits; ++k) {
-      const float w = exp2f(ld_cluster(in_cta(m_at + row * 4, k)) - ref);
-      l += w * ld_cluster(in_cta(l_at + row * 4, k));
-      const float4 v = ld_cluster4(in_cta(part_at + (row * D + c * 4) * 4, k));
-      sum.x = fmaf(w, v.x, sum.x);
-      sum.y = fmaf(w, v.y, sum.y);
-      sum.z = fmaf(w, v.z, sum.z);
-      sum.w = fmaf(w, v.w, sum.w);
-    }
+#pragma unroll
+    for (int k = 0; k < kMostSplits; ++k)
+      if (k < a.splits) {
+        const float w = exp2f(s_all_m[k][row] - ref);
+        l += w * s_all_l[k][row];
+        sum.x = fmaf(w, v[k].x, sum.x);
+        sum.y = fmaf(w, v[k].y, sum.y);
+        sum.z = fmaf(w, v[k].z, sum.z);
+        sum.w = fmaf(w, v[k].w, sum.w);
+      }
     for (int k = 0; k < a.num_parts; ++k) {
       const float2 ml = __ldcg(&a.part_ml[k * part_rows + part_row]);
       const float w = exp2f(ml.x - ref);

@@ -97,9 +97,7 @@ AttendKernel attend_tiles_of(int D, bool shared) {
 // Rows of a KV head and request up to which attend_rows takes them, if
 // attend_tiles could.
 constexpr int kMostNarrowRows = 64;
-// Splits of a unit's keys in a cluster, and the keys that a split should at
-// least have.
-constexpr int kMostSplits = 8;
+// Keys that a split of a unit's keys should at least have.
 constexpr int kKeysPerSplit = 128;
 // The shared prefix gets a grid of its own (attend_tiles over all requests'
 // rows) where the requests would otherwise read this many bytes of it.
@@ -144,7 +142,7 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   const int64_t keys = std::max<int64_t>(int64_t(a->max_blocks_per_req) * c->block_size, a->shared_len) -
                        (p.parts ? a->shared_len : 0);
   if (!p.wide)
-    while (p.splits < kMostSplits && p.units * q->kv_heads * p.splits < 2 * q->sm_count &&
+    while (p.splits < isq::kMostSplits && p.units * q->kv_heads * p.splits < 2 * q->sm_count &&
            keys >= int64_t(2 * p.splits) * kKeysPerSplit)
       p.splits *= 2;
   return p;
