@@ -74,26 +74,35 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Waits until the phase of the given parity has completed.  After the limit
-// (about two seconds), or once another thread has given up, returns false;
-// without a flag only the limit counts.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* failed) {
-  const uint32_t addr = smem_addr(bar);
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// The rest of a wait: gives up after about two seconds, or once another thread
+// has; without a flag only the limit counts.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int32_t* failed) {
   const long long began = clock64();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return true;
+  while (!bar_done(bar, parity)) {
     if (failed != nullptr && *failed) return false;
     if (clock64() - began > (1ll << 32)) {
       if (failed != nullptr) *failed = 1;
       return false;
     }
   }
+  return true;
+}
+// Waits until the phase of the given parity has completed, or returns false.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int32_t* failed) {
+  const uint32_t addr = smem_addr(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (bar_done(addr, parity)) return true;
+  return bar_wait_long(addr, parity, failed);
 }
 
 // True in one lane of a converged warp.  The compiler knows it for one lane, so
@@ -425,81 +434,72 @@ __device__ __forceinline__ uint32_t dims_at(int k) {
   return uint32_t((k >> 2) * kSlabStep + (k & 3) * 32);
 }
 
-constexpr int kGatherWarps = 4;
-
-// Warp g of kGatherWarps brings the tiles K0 V0 K1 V1 ... of keys [lo, hi) of
-// request r and KV head h into a ring of NS slots of kTileKeys x D.  full[]
-// take kGatherWarps arrivals, empty[] one (a product's commit).  A tile comes as
-// boxes, or key by key (keys outside [first_key, hi) as zeros) where a box
-// holds keys of two blocks and where there is no map; with ZERO_EDGE also
-// values that run past hi.  Boxes leave keys outside the range as they find
-// them.  A block outside the cache sets *bad, and its keys mean nothing.
-template <int D, int NS, bool ZERO_EDGE>
+// Warp g of W brings every W-th of the tiles K0 V0 K1 V1 ... of keys [lo, hi)
+// of request r and KV head h into a ring of NS slots of kTileKeys x D.  (A
+// tile's look-ups, waits and copies take one warp some 2000 cycles, mostly
+// latency, so whole tiles go to warps in turn.  W divides NS: a slot is always
+// the same warp's, which so sees every phase of its barriers.)  full[] and
+// empty[] take one arrival.  A tile comes as boxes, or key by key (keys outside
+// [first_key, hi) as zeros) where a box holds keys of two blocks and where
+// there is no map; with ZERO_EDGE also values that run past hi.  Boxes leave
+// keys outside the range as they find them.  A block outside the cache sets
+// *bad, and its keys mean nothing.
+template <int D, int NS, int W, bool ZERO_EDGE>
 __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map,
                                              int g, int32_t r, int32_t h, int32_t lo, int32_t hi, int32_t tiles,
                                              unsigned char* ring, uint64_t* full, uint64_t* empty,
                                              volatile int32_t* failed, int32_t* bad) {
-  constexpr int CPR = D / 8, kSlotBytes = kTileKeys * D * 2, kMostBoxes = kTileKeys / 8 / kGatherWarps;
+  constexpr int CPR = D / 8, kSlotBytes = kTileKeys * D * 2;
+  static_assert(NS % W == 0, "a slot belongs to one warp");
   const int lane = threadIdx.x & 31;
-  const int32_t bits = max(0, a.box_log2);
+  const int32_t bits = max(0, a.box_log2), boxes = kTileKeys >> bits;
   const int32_t slab = h * a.head_slabs;
   auto by_box = [&](int32_t j0, bool v) {
     const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys && (a.table_shared & ((1 << bits) - 1)) != 0;
     return a.box_log2 >= 0 && !torn && !(ZERO_EDGE && v && hi - j0 < kTileKeys);
   };
-  // This warp's boxes are g, g + kGatherWarps, ...; lane i looks up the i-th of
-  // them, a tile ahead of the copies that need it.
-  const int32_t my_key = (lane * kGatherWarps + g) << bits;
-  auto position = [&](int32_t t) -> int32_t {
-    const int32_t j0 = lo + t * kTileKeys;
-    return a.box_log2 >= 0 && t < tiles && lane < kMostBoxes && my_key < kTileKeys && hi - j0 > my_key ? j0 + my_key : -1;
+  // Lane i looks up box i of this warp's next tile (position -1: none), a tile
+  // ahead of the copies that need it.
+  int32_t next_pos, next_token, next_entry;
+  auto look_up = [&](int32_t t) {
+    const int32_t j0 = lo + t * kTileKeys, key = lane << bits;
+    next_pos = a.box_log2 >= 0 && t < tiles && lane < boxes && hi - j0 > key ? j0 + key : -1;
+    const int32_t jb = next_pos < 0 ? 0 : next_pos / a.block_size;
+    next_token = next_pos - jb * a.block_size;
+    const int32_t* from = a.q_offsets;  // (a load in every case: one under a condition would be waited for there)
+    if (next_pos >= 0)
+      from = next_pos < a.table_shared ? a.shared_blocks + jb : a.block_tables + int64_t(r) * a.max_blocks + jb;
+    next_entry = *from;
   };
-  // (a load in every case: one under a condition would be waited for there)
-  auto look_up = [&](int32_t pos) -> int32_t { return *(pos < 0 ? a.q_offsets : table_slot(a, r, pos)); };
-  int32_t next_pos = position(0), next_entry = look_up(next_pos);
-  int32_t block[kMostBoxes], group[kMostBoxes];
-  uint32_t good = 0;
-  if (g == 0 && lane == 0) {
-    fetch_map(k_map);
-    fetch_map(v_map);
-  }
-  int32_t u = 0;
-  for (; u < 2 * tiles; ++u) {
-    const int slot = u % NS;
-    const bool v = u & 1;
+  look_up(g / 2);
+  if (lane == 0) fetch_map(g & 1 ? v_map : k_map);
+  int32_t u = g;
+  for (; u < 2 * tiles; u += W) {
     const int32_t j0 = lo + (u >> 1) * kTileKeys;
-    if (!v) {
-      const int32_t pos = next_pos, entry = next_entry;
-      const bool fine = entry >= 0 && entry < a.num_blocks;
-      good = __ballot_sync(0xffffffffu, pos >= 0 && fine);
-      if (pos >= 0 && !fine && by_box(j0, false)) {
-        record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
-        *bad = 1;
-      }
-      const int32_t in_block = pos < 0 ? 0 : (pos % a.block_size) >> 3;
-#pragma unroll
-      for (int i = 0; i < kMostBoxes; ++i) {
-        block[i] = __shfl_sync(0xffffffffu, entry, i);
-        group[i] = __shfl_sync(0xffffffffu, in_block, i);
-      }
-      next_pos = position((u >> 1) + 1);
-      next_entry = look_up(next_pos);
+    const bool v = u & 1;
+    const CUtensorMap* map = v ? v_map : k_map;
+    const uint16_t* cache = v ? a.v_cache : a.k_cache;
+    const int slot = u % NS;
+    const uint32_t dst = smem_addr(ring + slot * kSlotBytes);
+    const int32_t pos = next_pos, entry = next_entry, group = next_token >> 3;
+    const bool boxed = by_box(j0, v), fine = entry >= 0 && entry < a.num_blocks;
+    const uint32_t good = __ballot_sync(0xffffffffu, pos >= 0 && fine);
+    if (pos >= 0 && !fine && boxed) {
+      record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
+      *bad = 1;
     }
+    look_up((u + W) >> 1);
     // the whole warp goes on or stops
     if (u >= NS && !__all_sync(0xffffffffu, bar_wait(&empty[slot], ((u / NS) - 1) & 1, failed))) break;
-    const uint32_t dst = smem_addr(ring + slot * kSlotBytes);
-    if (by_box(j0, v)) {
-      const CUtensorMap* map = v ? v_map : k_map;
-      if (elect_one()) {
-        bar_expect(&full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
-#pragma unroll
-        for (int i = 0; i < kMostBoxes; ++i)
-          if ((good >> i) & 1u)
-            copy_box(dst + ((i * kGatherWarps + g) << bits) * (D * 2), map, slab, group[i], block[i], &full[slot]);
+    if (boxed) {
+      if (elect_one()) bar_expect(&full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
+      for (int box = 0; box < boxes; ++box) {
+        const int32_t at_block = __shfl_sync(0xffffffffu, entry, box), at_group = __shfl_sync(0xffffffffu, group, box);
+        if (((good >> box) & 1u) && elect_one())
+          copy_box(dst + (box << bits) * (D * 2), map, slab, at_group, at_block, &full[slot]);
       }
     } else {
-      const uint16_t* cache = v ? a.v_cache : a.k_cache;
-      for (int first = 32 * g; first < kTileKeys; first += 32 * kGatherWarps) {
+      for (int first = 0; first < kTileKeys; first += 32) {
         const int32_t j = j0 + first + lane;
         int64_t at = -1;
         if (hi - j0 > first + lane && j >= a.first_key) {
@@ -521,7 +521,7 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
     }
   }
   if (*failed)  // copies in flight: nothing may leave before they land
-    for (int32_t i = max(0, u - NS); i < u; ++i) bar_wait(&full[i % NS], (i / NS) & 1, nullptr);
+    for (int32_t i = max(g, u - NS); i < u; i += W) bar_wait(&full[i % NS], (i / NS) & 1, nullptr);
 }
 
 // Queries of `rows` rows to a tile, zeros up to `count`, by `threads` threads.

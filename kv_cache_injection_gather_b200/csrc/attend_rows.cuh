@@ -28,8 +28,6 @@
 
 namespace isq {
 
-constexpr int kRowsThreads = (4 + kGatherWarps + 1) * 32;
-constexpr int kProductWarp = 4 + kGatherWarps;
 constexpr int kMostSplits = 8;  // CTAs of a cluster
 
 template <int D, int NR>
@@ -39,6 +37,9 @@ struct RowsShape {
 #define V_S128 6
 #endif
   static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR > 32 ? 5 : NR > 16 ? 6 : V_S128) : D == 64 ? 10 : 16;
+  static constexpr int kGather = kSlots == 16 ? 4 : kSlots == 10 ? 5 : kSlots;  // gather warps
+  static constexpr int kProductWarp = 4 + kGather;
+  static constexpr int kThreads = (4 + kGather + 1) * 32;
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kPBytes = NR * kTileKeys * 2;           // twice
   static constexpr int kRingBytes = kSlots * kSlotBytes;
@@ -51,11 +52,11 @@ struct RowsShape {
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 == 3) ? 2 : 1) attend_rows_kernel(
+__global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR == 16 && V_S128 == 3) ? 2 : 1) attend_rows_kernel(
     const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using S = RowsShape<D, NR>;
-  constexpr int CPR = D / 8, NS = S::kSlots;
+  constexpr int CPR = D / 8, NS = S::kSlots, NT = S::kThreads;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o, bar_end;
   __shared__ __align__(16) float s_m[NR];
@@ -72,14 +73,14 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
   const int32_t cluster = int32_t(blockIdx.x / a.splits);
   const int32_t h = cluster % a.kv_heads;
   if (cluster == gridDim.x / a.splits - 1) {
-    if (split == 0) check_requests<kRowsThreads>(a);
+    if (split == 0) check_requests<NT>(a);
     wait_for_previous();
     return;
   }
   // what needs no metadata first, beside the loads of find_unit
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], kGatherWarps);
+      bar_init(&bar_full[i], 1);
       bar_init(&bar_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -93,12 +94,12 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
     s_failed = 0;
     s_bad = 0;
   }
-  if (warp == kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
+  if (warp == S::kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   int32_t r, tile;
   Request rq;
-  find_unit<NR, kRowsThreads>(a, cluster / a.kv_heads, r, tile, rq);
+  find_unit<NR, NT>(a, cluster / a.kv_heads, r, tile, rq);
   if (r < 0) {  // so for the whole cluster
-    if (warp == kProductWarp) tmem_free(s_tmem, S::kColumns);
+    if (warp == S::kProductWarp) tmem_free(s_tmem, S::kColumns);
     wait_for_previous();  // on every path: the next grid relies on both
     return;
   }
@@ -134,10 +135,10 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
   const uint32_t tmem = s_tmem;               // S^T, twice NR columns
   const uint32_t tmem_o = tmem + 2 * NR;      // O^T, NR columns per 128 dims
 
-  if (warp >= 4 && warp < kProductWarp) {
-    gather_tiles<D, NS, false>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
+  if (warp >= 4 && warp < S::kProductWarp) {
+    gather_tiles<D, NS, S::kGather, false>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
                                &s_bad);
-  } else if (warp == kProductWarp) {
+  } else if (warp == S::kProductWarp) {
     // ---------------- products
     if (tiles > 0 && elect_one()) {
       bool ok = bar_wait(&bar_q, 0, &s_failed);
@@ -200,6 +201,13 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
       const int32_t j0 = lo + t * kTileKeys, j = j0 + tid;
       const bool edge = j0 < a.first_key || hi - j0 < kTileKeys;
       const bool in = j >= a.first_key && hi - j0 > tid;
+      ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_s[t & 1], (t >> 1) & 1, &s_failed));
+      tc_fence_after();
+      uint32_t v[NR];
+      if (ok) {
+        tmem_ld<NR>(tmem + (t & 1) * NR + lanes, v);
+        tmem_wait_ld();
+      }
       // Values of keys that take no part become zeros: their probabilities
       // are, and 0 * NaN is not.
       if (edge) {
@@ -210,13 +218,6 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
           for (int c = 0; c < CPR; ++c)
             *reinterpret_cast<uint4*>(row + tile_at<D>(tid, c)) = make_uint4(0, 0, 0, 0);
         }
-      }
-      ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_s[t & 1], (t >> 1) & 1, &s_failed));
-      tc_fence_after();
-      uint32_t v[NR];
-      if (ok) {
-        tmem_ld<NR>(tmem + (t & 1) * NR + lanes, v);
-        tmem_wait_ld();
       }
       const bool masked = edge || j0 + kTileKeys > lim_min;
       float x[NR];
@@ -260,6 +261,8 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
           s_shrink[tid] = top == neg_inf() ? 1.f : exp2_fast(old - top);
         }
         asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+        // (the sums up to t - 2 are done: their commit came before that of this
+        // tile's scores)
         if (t > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_o, (t - 1) & 1, &s_failed));
         if (t > 0 && ok) {
           tc_fence_after();
@@ -346,11 +349,11 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kProductWarp) {
+  if (warp == S::kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, S::kColumns);
   }
-  for (int row = warp; row < rows; row += kRowsThreads / 32) {
+  for (int row = warp; row < rows; row += NT / 32) {
     // keys past the row's limit, or of a bad block, were in its tiles
     if (!s_odd[row] || (s_lim[row] >= hi && s_bad == 0)) continue;
     float m, l, x[D / 32];
@@ -371,13 +374,13 @@ __global__ void __launch_bounds__(kRowsThreads, (D == 128 && NR == 16 && V_S128 
   wait_for_previous();
   const int64_t part_rows = int64_t(a.num_tokens) * a.num_heads;
   const uint32_t part_at = smem_addr(part), m_at = smem_addr(s_m), l_at = smem_addr(s_l);
-  for (int i = tid; i < rows * a.splits; i += kRowsThreads) {
+  for (int i = tid; i < rows * a.splits; i += NT) {
     const int row = i % rows, k = i / rows;
     s_all_m[k][row] = ld_cluster(in_cta(m_at + row * 4, k));
     s_all_l[k][row] = ld_cluster(in_cta(l_at + row * 4, k));
   }
   __syncthreads();
-  for (int i = split * kRowsThreads + tid; i < rows * (D / 4); i += kRowsThreads * a.splits) {
+  for (int i = split * NT + tid; i < rows * (D / 4); i += NT * a.splits) {
     const int row = i / (D / 4), c = i % (D / 4);
     const int64_t t = rq.tok0 + token_of(row);
     const int32_t head = head_of(row);

@@ -15,10 +15,10 @@
 // smaller one gives both streams the same rows and every other key tile, and
 // their sums are joined at the end.
 //
-// Warps 0-3 and 4-7 do the streams' softmax, one row a thread; warps 8-11
+// Warps 0-3 and 4-7 do the streams' softmax, one row a thread; warps 8 on
 // gather keys and values from the cache's blocks into a ring of 128-key tiles
 // (TMA boxes of a block's tokens, in the 128-byte swizzle that the products
-// read); one thread of warp 12 issues the products.  mbarriers join them.  Every wait is
+// read); one thread of the last issues the products.  mbarriers join them.  Every wait is
 // bounded: a thread that gives up sets a flag that all see, the CTA drains,
 // frees its tensor memory and records IS_ERR_TIMEOUT.
 #pragma once
@@ -29,12 +29,14 @@ namespace isq {
 
 constexpr int kStreamRows = 128;
 constexpr int kUnitRows = 2 * kStreamRows;
-constexpr int kTilesThreads = (8 + kGatherWarps + 1) * 32;
 
 template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kGather = D == 128 ? 5 : 4;       // gather warps
+  static constexpr int kProductWarp = 8 + kGather;
+  static constexpr int kThreads = (8 + kGather + 1) * 32;
   static constexpr int kQBytes = kUnitRows * D * 2;
   // data, and up to 1 KB to align it
   static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
@@ -62,7 +64,7 @@ __device__ __forceinline__ int32_t owner_of(const AttendArgs& a, int32_t t) {
 // a.part_o is set, split s of a unit's keys goes to part s of the work space;
 // otherwise there is one split and it goes to the output.
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
+__global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kernel(
     const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using S = TilesShape<D>;
@@ -87,10 +89,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
     rq = {0, a.num_tokens, 0, 0};
   } else {
     if (blockIdx.x == gridDim.x - 1) {
-      check_requests<kTilesThreads>(a);
+      check_requests<S::kThreads>(a);
       return;
     }
-    find_unit<kUnitRows, kTilesThreads>(a, unit, r, tile, rq);
+    find_unit<kUnitRows, S::kThreads>(a, unit, r, tile, rq);
     if (r < 0) return;
   }
 
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], kGatherWarps);
+      bar_init(&bar_full[i], 1);
       bar_init(&bar_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
     s_failed = 0;
     s_bad = 0;
   }
-  if (warp == 12) tmem_alloc(&s_tmem, 512);
+  if (warp == S::kProductWarp) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -144,10 +146,10 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
   float m = neg_inf(), l = 0.f;  // softmax warps: of this thread's row
   int32_t lim = 0;
 
-  if (warp >= 8 && warp < 12) {
-    gather_tiles<D, NS, true>(a, &k_map, &v_map, warp - 8, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
+  if (warp >= 8 && warp < S::kProductWarp) {
+    gather_tiles<D, NS, S::kGather, true>(a, &k_map, &v_map, warp - 8, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
                               &s_bad);
-  } else if (warp == 12) {
+  } else if (warp == S::kProductWarp) {
     // ---------------- products
     if (elect_one()) {
       bool ok = true;
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1) attend_tiles_kernel(
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == S::kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }

@@ -66,7 +66,7 @@ struct AttendKernel {
 // The streaming kernel for units of 16, 32 or 64 rows (head_dim 256: 16).
 template <int D, int NR>
 AttendKernel attend_rows_of() {
-  return {&isq::attend_rows_kernel<D, NR>, isq::RowsShape<D, NR>::kSmemBytes, isq::kRowsThreads, NR};
+  return {&isq::attend_rows_kernel<D, NR>, isq::RowsShape<D, NR>::kSmemBytes, isq::RowsShape<D, NR>::kThreads, NR};
 }
 template <int D>
 AttendKernel attend_rows_of(int64_t most) {
@@ -86,7 +86,7 @@ AttendKernel attend_rows_of(int D, int64_t most) {
 template <int D>
 AttendKernel attend_tiles_of(bool shared) {
   return {shared ? &isq::attend_tiles_kernel<D, true> : &isq::attend_tiles_kernel<D, false>,
-          isq::TilesShape<D>::kSmemBytes, isq::kTilesThreads, isq::kUnitRows};
+          isq::TilesShape<D>::kSmemBytes, isq::TilesShape<D>::kThreads, isq::kUnitRows};
 }
 AttendKernel attend_tiles_of(int D, bool shared) {
   if (D == 64) return attend_tiles_of<64>(shared);
