@@ -20,7 +20,9 @@ struct AttendArgs {
   const int32_t* shared_blocks;
   int32_t shared_len;
   int32_t causal;
-  int32_t splits;              // CTAs that share a unit's keys
+  int64_t units;               // attend_rows: units of its grid
+  int32_t splits;              // CTAs that share a unit's keys; attend_rows: a
+  int32_t splits_log2;         // cluster of 1, 2, 4 or 8
   // Parts of the rows' sums in the work space, each [num_tokens][num_heads]:
   // (maximum, sum) pairs and [D] sums of values, all fp32.  attend_tiles
   // writes part `split`; attend_rows reads `num_parts` of them.
@@ -270,27 +272,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Address of the same shared variable in another CTA of the cluster.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
 // ---------------------------------------------------------------- requests
@@ -493,10 +487,19 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
     if (u >= NS && !__all_sync(0xffffffffu, bar_wait(&empty[slot], ((u / NS) - 1) & 1, failed))) break;
     if (boxed) {
       if (elect_one()) bar_expect(&full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
-      for (int box = 0; box < boxes; ++box) {
-        const int32_t at_block = __shfl_sync(0xffffffffu, entry, box), at_group = __shfl_sync(0xffffffffu, group, box);
-        if (((good >> box) & 1u) && elect_one())
-          copy_box(dst + (box << bits) * (D * 2), map, slab, at_group, at_block, &full[slot]);
+      for (int box = 0; box < boxes; box += 8) {
+        int32_t at_block[8], at_group[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          at_block[i] = __shfl_sync(0xffffffffu, entry, box + i);
+          at_group[i] = __shfl_sync(0xffffffffu, group, box + i);
+        }
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((good >> (box + i)) & 1u)
+              copy_box(dst + ((box + i) << bits) * (D * 2), map, slab, at_group[i], at_block[i], &full[slot]);
+        }
       }
     } else {
       for (int first = 0; first < kTileKeys; first += 32) {

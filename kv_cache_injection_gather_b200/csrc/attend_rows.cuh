@@ -28,31 +28,30 @@
 
 namespace isq {
 
-constexpr int kMostSplits = 8;  // CTAs of a cluster
+constexpr int kMostSplits = 8;   // CTAs of a cluster
 
 template <int D, int NR>
 struct RowsShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;         // one K or V tile
-#ifndef V_S128
-#define V_S128 6
-#endif
-  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR > 32 ? 5 : NR > 16 ? 6 : V_S128) : D == 64 ? 10 : 16;
-  static constexpr int kGather = kSlots == 16 ? 4 : kSlots == 10 ? 5 : kSlots;  // gather warps
+  // As many slots as fit, and gather warps that divide them; with 64 rows as
+  // few warps as leave the softmax its registers.
+  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR == 16 ? 6 : NR == 32 ? 5 : 4) : D == 64 ? 10 : 16;
+  static constexpr int kGather = NR == 64 ? 2 : kSlots == 16 ? 4 : kSlots == 10 ? 5 : kSlots;
   static constexpr int kProductWarp = 4 + kGather;
   static constexpr int kThreads = (4 + kGather + 1) * 32;
   static constexpr int kQBytes = NR * D * 2;
   static constexpr int kPBytes = NR * kTileKeys * 2;           // twice
+  static constexpr int kJoinBytes = NR * D * 4;                // the cluster's sums of this CTA's dims
   static constexpr int kRingBytes = kSlots * kSlotBytes;
-  static constexpr int kSmemBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024 + 2 * kPBytes + 1024;
+  static constexpr int kSmemBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024 + 2 * kPBytes + kJoinBytes + 1024;
   static constexpr int kGroups = (D + 127) / 128;              // O^T accumulators
   // S^T twice and O^T, as a power of two of columns
   static constexpr int kColumns = NR == 16 ? 64 : NR == 32 ? 128 : 256;
   static_assert((2 + kGroups) * NR <= kColumns, "tensor memory");
-  static_assert(NR * D * 4 <= kRingBytes, "the sums fit over the ring");
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR == 16 && V_S128 == 3) ? 2 : 1) attend_rows_kernel(
+__global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_kernel(
     const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap k_map,
     const __grid_constant__ CUtensorMap v_map) {
   using S = RowsShape<D, NR>;
@@ -61,22 +60,24 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o, bar_end;
   __shared__ __align__(16) float s_m[NR];
   __shared__ __align__(16) float s_top[4][NR], s_shrink[NR];
-  __shared__ float s_l[NR], s_all_m[kMostSplits][NR], s_all_l[kMostSplits][NR];
+  __shared__ float s_l[NR];
+  __shared__ __align__(8) float2 s_join_ml[kMostSplits][NR];  // of the cluster's CTAs
   __shared__ int32_t s_lim[NR], s_odd[NR];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
-  // grid: (unit, KV head, split), the splits of a unit and head a cluster; the
-  // cluster after the last checks the batch
-  const int32_t split = int32_t(blockIdx.x % a.splits);
-  const int32_t cluster = int32_t(blockIdx.x / a.splits);
-  const int32_t h = cluster % a.kv_heads;
-  if (cluster == gridDim.x / a.splits - 1) {
-    if (split == 0) check_requests<NT>(a);
+  // grid: x (KV head, split), the splits of a unit and head a cluster; y and z
+  // the unit, of which the one after the last checks the batch
+  const int32_t split = int32_t(blockIdx.x) & (a.splits - 1);
+  const int32_t h = int32_t(blockIdx.x >> a.splits_log2);
+  const int64_t unit = int64_t(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (unit >= a.units) {
+    if (unit == a.units && blockIdx.x == 0) check_requests<NT>(a);
     wait_for_previous();
     return;
   }
+  if (a.splits > 1) cluster_arrive();  // this CTA has started: its shared memory may be written
   // what needs no metadata first, beside the loads of find_unit
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -97,9 +98,10 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
   if (warp == S::kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   int32_t r, tile;
   Request rq;
-  find_unit<NR, NT>(a, cluster / a.kv_heads, r, tile, rq);
+  find_unit<NR, NT>(a, int32_t(unit), r, tile, rq);
   if (r < 0) {  // so for the whole cluster
     if (warp == S::kProductWarp) tmem_free(s_tmem, S::kColumns);
+    if (a.splits > 1) cluster_wait();
     wait_for_previous();  // on every path: the next grid relies on both
     return;
   }
@@ -112,14 +114,16 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
   // tiles, from a box's border on (the keys below first_key are left out)
   const int32_t begin = a.box_log2 < 0 ? a.first_key : a.first_key >> a.box_log2 << a.box_log2;
   const int32_t end = row_limit(a, rq, token_of(rows - 1));
-  const int64_t all_tiles = end > a.first_key ? (int64_t(end) - begin + kTileKeys - 1) / kTileKeys : 0;
-  const int32_t lo = begin + int32_t(all_tiles * split / a.splits) * kTileKeys;
-  const int32_t hi = int32_t(min(int64_t(end), begin + all_tiles * (split + 1) / a.splits * kTileKeys));
+  const int32_t all_tiles = end > a.first_key ? int32_t(uint32_t(end - begin + kTileKeys - 1) / kTileKeys) : 0;
+  const int32_t lo = begin + (all_tiles * split >> a.splits_log2) * kTileKeys;
+  const int32_t last = all_tiles * (split + 1) >> a.splits_log2;
+  const int32_t hi = all_tiles == 0 ? lo : last == all_tiles ? end : begin + last * kTileKeys;
   const int32_t tiles = hi > lo ? (hi - lo + kTileKeys - 1) / kTileKeys : 0;
 
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* p_tiles = ring + S::kRingBytes;
-  unsigned char* q_tile = p_tiles + 2 * S::kPBytes;
+  float* join_o = reinterpret_cast<float*>(p_tiles + 2 * S::kPBytes);  // [split][row][D / splits]
+  unsigned char* q_tile = p_tiles + 2 * S::kPBytes + S::kJoinBytes;
 
   if (tid < NR) {
     s_lim[tid] = tid < rows ? min(hi, row_limit(a, rq, token_of(tid))) : hi;
@@ -323,27 +327,25 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
     __syncwarp();
   }
   tc_fence_before();
-  __syncthreads();  // every slot of the ring is free
+  __syncthreads();
   tc_fence_after();
-  float* part = reinterpret_cast<float*>(ring);  // [row][D]
+  // a row is odd if its sums are not finite and keys past its limit were in
+  // its tiles, or if a block was bad: it is summed again key by key
+  uint32_t o[S::kGroups][NR];
   if (warp < 4) {
     if (tid < rows) s_l[tid] = s_top[0][tid] + s_top[1][tid] + s_top[2][tid] + s_top[3][tid];
-#pragma unroll 1
-    for (int g = 0; g < S::kGroups; ++g) {
-      uint32_t v[NR];
-      if (tiles > 0) {
-        tmem_ld<NR>(tmem_o + g * NR + (uint32_t(warp) << 21), v);
-        tmem_wait_ld();
-      }
-      const int d = g * 128 + tid;
 #pragma unroll
-      for (int c = 0; c < NR; ++c) {
-        const float x = tiles > 0 ? __uint_as_float(v[c]) : 0.f;
-        if (c < rows && d < D) {
-          part[c * D + d] = x;
-          if (!finite(x)) s_odd[c] = 1;
-        }
+    for (int g = 0; g < S::kGroups; ++g) {
+      if (tiles > 0) {
+        tmem_ld<NR>(tmem_o + g * NR + (uint32_t(warp) << 21), o[g]);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int c = 0; c < NR; ++c) o[g][c] = 0;
       }
+#pragma unroll
+      for (int c = 0; c < NR; ++c)
+        if (c < rows && g * 128 + tid < D && !finite(__uint_as_float(o[g][c])) && s_lim[c] < hi) s_odd[c] = 1;
     }
     if (s_bad != 0 && tid < rows) s_odd[tid] = 1;
   }
@@ -353,66 +355,75 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
     tc_fence_after();
     tmem_free(tmem, S::kColumns);
   }
+
+  // ---- join the splits: CTA k of the cluster gets everybody's maxima and sums
+  // and the k-th share of the dims, written into its shared memory
+  if (a.splits > 1) cluster_wait();  // they have all started
+  constexpr int kLogD = D == 256 ? 8 : D == 128 ? 7 : D == 64 ? 6 : 5;
+  const int share_log2 = kLogD - a.splits_log2, share = 1 << share_log2;
+  const uint32_t o_at = smem_addr(join_o), ml_at = smem_addr(s_join_ml);
+  auto join_at = [&](int row, int d) {  // of (row, dim d) in the CTA that gets it
+    return in_cta(o_at + ((((split * NR + row) << share_log2) + (d & (share - 1))) << 2), d >> share_log2);
+  };
+  auto join_ml = [&](int row, float m, float l, int to) {
+    st_cluster2(in_cta(ml_at + (split * NR + row) * 8, to), m, l);
+  };
+  if (warp < 4) {
+#pragma unroll
+    for (int g = 0; g < S::kGroups; ++g)
+#pragma unroll
+      for (int c = 0; c < NR; ++c)
+        if (c < rows && g * 128 + tid < D && !s_odd[c]) st_cluster(join_at(c, g * 128 + tid), __uint_as_float(o[g][c]));
+  } else {
+    for (int i = tid - 128; i < rows << a.splits_log2; i += NT - 128) {
+      const int row = i >> a.splits_log2;
+      if (!s_odd[row]) join_ml(row, s_m[row], s_l[row], i & (a.splits - 1));
+    }
+  }
   for (int row = warp; row < rows; row += NT / 32) {
-    // keys past the row's limit, or of a bad block, were in its tiles
-    if (!s_odd[row] || (s_lim[row] >= hi && s_bad == 0)) continue;
+    if (!s_odd[row]) continue;
     float m, l, x[D / 32];
     row_by_keys<D>(a, r, h, a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs,
                    max(lo, a.first_key), s_lim[row], m, l, x);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) part[row * D + lane + 32 * i] = x[i];
-    if (lane == 0) {
-      s_m[row] = m;
-      s_l[row] = l;
-    }
+    for (int i = 0; i < D / 32; ++i) st_cluster(join_at(row, lane + 32 * i), x[i]);
+    if (lane < a.splits) join_ml(row, m, l, lane);
   }
-
-  // ---- join the splits' sums, and the parts of the grid before: each CTA of
-  // the cluster a share of the rows' vectors, read from all of them
-  if (a.splits > 1) cluster_sync();
-  else __syncthreads();
+  if (a.splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
   wait_for_previous();
   const int64_t part_rows = int64_t(a.num_tokens) * a.num_heads;
-  const uint32_t part_at = smem_addr(part), m_at = smem_addr(s_m), l_at = smem_addr(s_l);
-  for (int i = tid; i < rows * a.splits; i += NT) {
-    const int row = i % rows, k = i / rows;
-    s_all_m[k][row] = ld_cluster(in_cta(m_at + row * 4, k));
-    s_all_l[k][row] = ld_cluster(in_cta(l_at + row * 4, k));
-  }
-  __syncthreads();
-  for (int i = split * NT + tid; i < rows * (D / 4); i += NT * a.splits) {
-    const int row = i / (D / 4), c = i % (D / 4);
+  for (int i = tid; i < rows << (share_log2 - 2); i += NT) {
+    const int row = i >> (share_log2 - 2), c = (i << 2) & (share - 1);
     const int64_t t = rq.tok0 + token_of(row);
-    const int32_t head = head_of(row);
+    const int32_t head = head_of(row), d = split * share + c;
     const int64_t part_row = t * a.num_heads + head;
-    float4 v[kMostSplits];
     float m = neg_inf();
-#pragma unroll
-    for (int k = 0; k < kMostSplits; ++k)
-      if (k < a.splits) {
-        v[k] = ld_cluster4(in_cta(part_at + (row * D + c * 4) * 4, k));
-        m = fmaxf(m, s_all_m[k][row]);
-      }
+    for (int k = 0; k < a.splits; ++k) m = fmaxf(m, s_join_ml[k][row].x);
     for (int k = 0; k < a.num_parts; ++k) m = fmaxf(m, __ldcg(&a.part_ml[k * part_rows + part_row].x));
     const float ref = m == neg_inf() ? 0.f : m;
     float l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kMostSplits; ++k)
-      if (k < a.splits) {
-        const float w = exp2f(s_all_m[k][row] - ref);
-        l += w * s_all_l[k][row];
-        sum.x = fmaf(w, v[k].x, sum.x);
-        sum.y = fmaf(w, v[k].y, sum.y);
-        sum.z = fmaf(w, v[k].z, sum.z);
-        sum.w = fmaf(w, v[k].w, sum.w);
-      }
+    for (int k = 0; k < a.splits; ++k) {
+      const float2 ml = s_join_ml[k][row];
+      const float w = exp2f(ml.x - ref);
+      const float4 v = *reinterpret_cast<const float4*>(join_o + ((k * NR + row) << share_log2) + c);
+      l += w * ml.y;
+      sum.x = fmaf(w, v.x, sum.x);
+      sum.y = fmaf(w, v.y, sum.y);
+      sum.z = fmaf(w, v.z, sum.z);
+      sum.w = fmaf(w, v.w, sum.w);
+    }
     for (int k = 0; k < a.num_parts; ++k) {
       const float2 ml = __ldcg(&a.part_ml[k * part_rows + part_row]);
       const float w = exp2f(ml.x - ref);
       if (ml.y == 0.f) continue;  // nothing seen: the part's values mean nothing
       l += w * ml.y;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (k * part_rows + part_row) * D + c * 4));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (k * part_rows + part_row) * D + d));
       sum.x = fmaf(w, v.x, sum.x);
       sum.y = fmaf(w, v.y, sum.y);
       sum.z = fmaf(w, v.z, sum.z);
@@ -422,12 +433,11 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, (D == 128 && NR ==
     const bool none = l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
     if (none) sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<uint2*>(a.out.data + t * a.out.ts + head * a.out.hs + c * 4) =
+    *reinterpret_cast<uint2*>(a.out.data + t * a.out.ts + head * a.out.hs + d) =
         make_uint2(to_bf16x2(sum.x * inv, sum.y * inv), to_bf16x2(sum.z * inv, sum.w * inv));
-    if (a.lse != nullptr && c == 0) a.lse[part_row] = none ? neg_inf() : (m + log2f(l)) * kLn2;
+    if (a.lse != nullptr && d == 0) a.lse[part_row] = none ? neg_inf() : (m + log2f(l)) * kLn2;
   }
   if (s_failed && tid == 0) record(a.st, kErrTimeout, r);
-  if (a.splits > 1) cluster_sync();  // no CTA leaves while another reads it
 }
 
 }  // namespace isq

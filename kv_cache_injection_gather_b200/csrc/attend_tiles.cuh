@@ -110,9 +110,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   };
   // keys [lo, hi) of this CTA: whole tiles but the last
   const int32_t all = SHARED ? a.shared_len : limit_of(rows - 1);
-  const int64_t all_tiles = (int64_t(all) + kTileKeys - 1) / kTileKeys;
+  const uint32_t all_tiles = (uint32_t(all) + kTileKeys - 1) / kTileKeys;  // up to 2^24, times up to 16 splits
   const int32_t lo = int32_t(all_tiles * split / a.splits) * kTileKeys;
-  const int32_t hi = int32_t(min(int64_t(all), all_tiles * (split + 1) / a.splits * kTileKeys));
+  const uint32_t last = all_tiles * (split + 1) / a.splits;
+  const int32_t hi = last == all_tiles ? all : int32_t(last) * kTileKeys;
   const int32_t tiles = hi > lo ? (hi - lo + kTileKeys - 1) / kTileKeys : 0;
   const bool by_rows = rows > kStreamRows;
   const int32_t work = by_rows ? 2 * tiles : tiles;  // products S, streams in turn

@@ -395,9 +395,12 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return IS_ERR_INVALID_ARG;
     if (workspace_bytes < p.ml_bytes + p.o_bytes) return IS_ERR_CAPACITY;
   }
-  const int64_t grid = (p.units * query->kv_heads + 1) * p.splits;
+  // attend_tiles: one dimension; attend_rows: (head, split), units, more units
   const int64_t shared_grid = p.shared_units * query->kv_heads * p.parts;
-  if (grid > INT32_MAX || shared_grid > INT32_MAX) return IS_ERR_CAPACITY;
+  const int64_t grid_x = p.wide ? p.units * query->kv_heads + 1 : int64_t(query->kv_heads) * p.splits;
+  const int64_t grid_y = p.wide ? 1 : std::min<int64_t>(p.units + 1, 32768);
+  const int64_t grid_z = p.wide ? 1 : (p.units + grid_y) / grid_y;
+  if (grid_x > INT32_MAX || shared_grid > INT32_MAX || grid_z > 65535) return IS_ERR_CAPACITY;
   OnDevice guard(query->device);
   isq::AttendArgs a{};
   a.num_tokens = args->num_tokens;
@@ -454,13 +457,15 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
     a.first_key = a.shared_len;
     a.table_shared = 0;  // what is left of a request is in its own blocks
   }
+  a.units = p.units;
   a.splits = p.splits;
+  while ((1 << a.splits_log2) < p.splits) ++a.splits_log2;
   if (!p.wide && p.splits > 1) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.splits), 1, 1};
   }
   const AttendKernel& k = p.kernel;
-  cfg.gridDim = dim3(unsigned(grid));
+  cfg.gridDim = dim3(unsigned(grid_x), unsigned(grid_y), unsigned(grid_z));
   cfg.blockDim = dim3(unsigned(k.threads));
   cfg.dynamicSmemBytes = size_t(k.smem);
   if (cudaLaunchKernelEx(&cfg, k.fn, a, k_map, v_map) != cudaSuccess) {
