@@ -28,20 +28,23 @@ def _i32(t: torch.Tensor, name: str) -> torch.Tensor:
 
 def _rows(t: torch.Tensor, name: str, heads: int | None, D: int, T: int, device: int) -> B.is_rows_t:
     """bf16 [T][heads][D] on the device, any strides but the innermost (1)."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be bf16 [tokens][heads][{D}] with unit last stride")
-    n, h, d = t.shape
-    if n != T or d != D or (heads is not None and h != heads):
-        raise ValueError(f"{name} is {tuple(t.shape)}: expected ({T}, {'heads' if heads is None else heads}, {D})")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is not on cuda:{device}")
-    return B.is_rows_t(t.data_ptr(), t.stride(0), t.stride(1), h)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or stride[2] != 1 or t.dtype is not torch.bfloat16 \
+            or (heads is not None and shape[1] != heads) or t.get_device() != device:
+        raise ValueError(f"{name} must be bf16 [{T}][{'heads' if heads is None else heads}][{D}] with unit last "
+                         f"stride on cuda:{device}: got {t.dtype} {tuple(shape)}, strides {stride}, {t.device}")
+    return B.is_rows_t(t.data_ptr(), stride[0], stride[1], shape[1])
 
 
 def _ints(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, device: int) -> int:
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous() or t.get_device() != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on cuda:{device}")
     return t.data_ptr()
+
+
+# the current stream's address without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
+    or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 class _DeviceArray:
@@ -293,13 +296,12 @@ class FactStore:
     def _weight(self, w: torch.Tensor | None, name: str) -> int | None:
         if w is None:
             return None
-        if w.dtype is not torch.bfloat16 or w.dim() != 1 or w.shape[0] != self.D or not w.is_contiguous() \
-                or w.get_device() != self.device:
+        if w.dtype is not torch.bfloat16 or w.shape != (self.D,) or w.stride() != (1,) or w.get_device() != self.device:
             raise ValueError(f"{name} must be a contiguous bf16 [{self.D}] tensor on cuda:{self.device}")
         return w.data_ptr()
 
     def _stream(self, stream: int | None) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        return _raw_stream(self.device) if stream is None else stream
 
     def _empty(self, shape, dtype: torch.dtype, stream: int | None) -> torch.Tensor:
         """A new tensor whose memory belongs to the stream that writes it."""
