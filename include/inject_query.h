@@ -70,7 +70,7 @@ typedef struct {
  * number of heads and may be the input itself (same data and strides);
  * otherwise no output may overlap an input.  k (with k_out) may be NULL.
  *   positions   device int32 [num_tokens]; a negative one marks a padding
- *               token, whose rows are neither read nor written
+ *               token, whose rows are not written
  *   q_weight, k_weight   device bf16 [D], 16-byte aligned, or NULL
  *   eps         finite and >= 0, one for both
  * Errors: INVALID_ARG, CUDA.  num_tokens may be 0. */

@@ -47,14 +47,19 @@ void free_query(is_query* q) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Kernel tables over (head_dim, RoPE style) and head_dim.
+// Kernel tables over head_dim and its variants.
 using RowsKernel = void (*)(isq::RowArgs);
-RowsKernel rows_kernel_of(int D, int style) {
+template <int D>
+RowsKernel rows_kernel_of(int style, bool norm) {
+  if (style) return norm ? &isq::rows_kernel<D, 1, true> : &isq::rows_kernel<D, 1, false>;
+  return norm ? &isq::rows_kernel<D, 0, true> : &isq::rows_kernel<D, 0, false>;
+}
+RowsKernel rows_kernel_of(int D, int style, bool norm) {
   switch (D) {
-    case 32: return style ? &isq::rows_kernel<32, 1> : &isq::rows_kernel<32, 0>;
-    case 64: return style ? &isq::rows_kernel<64, 1> : &isq::rows_kernel<64, 0>;
-    case 128: return style ? &isq::rows_kernel<128, 1> : &isq::rows_kernel<128, 0>;
-    case 256: return style ? &isq::rows_kernel<256, 1> : &isq::rows_kernel<256, 0>;
+    case 32: return rows_kernel_of<32>(style, norm);
+    case 64: return rows_kernel_of<64>(style, norm);
+    case 128: return rows_kernel_of<128>(style, norm);
+    case 256: return rows_kernel_of<256>(style, norm);
     default: return nullptr;
   }
 }
@@ -195,11 +200,16 @@ int box_maps(const is_query* q, isq::AttendArgs& a, CUtensorMap& k, CUtensorMap&
   return box;
 }
 
+#ifndef V_NT
+#define V_NT 64
+#endif
 int launch_rows(const is_query* q, const isq::RowArgs& a, int32_t num_tokens, cudaStream_t st) {
-  const int per_row = q->head_dim / 16;
-  const int64_t want = int64_t(a.nq + a.nk + a.nv) * per_row;
-  const int threads = int(std::min<int64_t>((want + 31) / 32 * 32, isq::kRowThreads));
-  rows_kernel_of(q->head_dim, q->style)<<<unsigned(num_tokens), unsigned(threads), 0, st>>>(a);
+  const int64_t want = (int64_t(std::max({a.nq, a.nk, a.nv})) * (q->head_dim / 16) + 31) / 32 * 32;
+  // few tokens: a thread a row, for latency; many: threads with several rows
+  const int most = num_tokens < 4 * q->sm_count ? isq::kRowThreads : V_NT;
+  const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
+  const unsigned threads = unsigned(std::min<int64_t>(want, most));
+  rows_kernel_of(q->head_dim, q->style, norm)<<<unsigned(num_tokens), threads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
 }
 
@@ -237,7 +247,7 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
       (!(c.scale_factor > 0) || !(c.low_freq_factor > 0) || !(c.high_freq_factor > c.low_freq_factor) ||
        c.original_max_position < 1))
     return IS_ERR_INVALID_ARG;
-  if (!rows_kernel_of(c.head_dim, 0)) return IS_ERR_NOT_SUPPORTED;
+  if (!rows_kernel_of(c.head_dim, 0, false)) return IS_ERR_NOT_SUPPORTED;
   int ndev = 0;
   if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) {
     cudaGetLastError();
@@ -261,8 +271,10 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
   // Attributes now, so that the calls are launches alone (the functions are
   // loaded here, not inside somebody's stream capture).
   cudaFuncAttributes attr;
-  bool ok = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(rows_kernel_of(c.head_dim, c.rope_style))) ==
-            cudaSuccess;
+  bool ok = true;
+  for (bool norm : {false, true})
+    ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(
+                                                rows_kernel_of(c.head_dim, c.rope_style, norm))) == cudaSuccess;
   for (const AttendKernel& k : {attend_rows_of(c.head_dim, 16), attend_rows_of(c.head_dim, 32),
                                 attend_rows_of(c.head_dim, 64), attend_tiles_of(c.head_dim, false),
                                 attend_tiles_of(c.head_dim, true)})

@@ -106,138 +106,216 @@ __device__ __forceinline__ float2 cos_sin(int32_t position, double turns) {
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void st16(uint16_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
-__device__ __forceinline__ void unpack(const uint4& u, float* x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Two fp32 values in one 64-bit register, for the packed multiply and fused
+// multiply-add.
+using Two = uint64_t;
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two from_bf16x2(uint32_t w) { return two(lo_f(w), hi_f(w)); }
+__device__ __forceinline__ uint32_t to_bf16x2(Two v) {
+  const float2 f = both(v);
+  return to_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ Two swapped(Two v) {
+  const float2 f = both(v);
+  return two(f.y, f.x);
+}
+constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
+
+struct Vecs {
+  uint4 lo, hi;  // the 16-byte vectors c and c + D/16 of a row
+};
+template <int D>
+__device__ __forceinline__ Vecs load_row(const uint16_t* p) {
+  return {ld16(p), ld16(p + D / 2)};
+}
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* p, const Vecs& v) {
+  st16(p, v.lo);
+  st16(p + D / 2, v.hi);
+}
+
+// A thread's share of a rotation: two pairs a step, 4 steps.  With `x` the
+// step's two words (rotate-half: elements 2j, 2j + 1 of both vectors; adjacent:
+// words 2j and 2j + 1 of the 8), the results are x0 p[j][0] + other p[j][1] and
+// x1 p[j][2] + other p[j][3], where `other` is the other word (rotate-half) or
+// the word itself with its halves exchanged (adjacent).
+struct Rotation {
+  Two p[4][4];
+};
+template <int STYLE>
+__device__ __forceinline__ void set_rotation(Rotation& r, const float4* cs, int step, const Vecs& g) {
+  const uint32_t g0[4] = {g.lo.x, g.lo.y, g.lo.z, g.lo.w}, g1[4] = {g.hi.x, g.hi.y, g.hi.z, g.hi.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = lo_f(w[i]);
-    x[2 * i + 1] = hi_f(w[i]);
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = cs[j * step];  // cos, cos, sin, sin of pairs 2j, 2j + 1 of this thread
+    if constexpr (STYLE == 0) {
+      const Two co = two(v.x, v.y), si = two(v.z, v.w), wa = from_bf16x2(g0[j]), wb = from_bf16x2(g1[j]);
+      r.p[j][0] = mul(co, wa);
+      r.p[j][1] = mul(two(-v.z, -v.w), wb);
+      r.p[j][2] = mul(co, wb);
+      r.p[j][3] = mul(si, wa);
+    } else {
+      const Two wa = from_bf16x2(j < 2 ? g0[2 * j] : g1[2 * j - 4]), wb = from_bf16x2(j < 2 ? g0[2 * j + 1] : g1[2 * j - 3]);
+      r.p[j][0] = mul(two(v.x, v.x), wa);
+      r.p[j][1] = mul(two(-v.z, v.z), swapped(wa));
+      r.p[j][2] = mul(two(v.y, v.y), wb);
+      r.p[j][3] = mul(two(-v.w, v.w), swapped(wb));
+    }
   }
 }
 
-__device__ __forceinline__ uint4 pack(const float* x) {
-  return make_uint4(to_bf16x2(x[0], x[1]), to_bf16x2(x[2], x[3]), to_bf16x2(x[4], x[5]), to_bf16x2(x[6], x[7]));
+// Norm (with eps, over the row's threads) and rotation of a row.
+template <int D, int STYLE, bool NORM>
+__device__ __forceinline__ Vecs turn_row(const Vecs& in, const Rotation& rot, bool normed, float eps) {
+  constexpr int TPR = D / 16;
+  const uint32_t u[8] = {in.lo.x, in.lo.y, in.lo.z, in.lo.w, in.hi.x, in.hi.y, in.hi.z, in.hi.w};
+  Two x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = from_bf16x2(u[i]);
+  if (NORM && normed) {
+    Two sq = mul(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+    const float2 f = both(sq);
+    float sum = f.x + f.y;
+    const unsigned group = ((1u << TPR) - 1u) << ((threadIdx.x & 31) / TPR * TPR);
+#pragma unroll
+    for (int m = TPR / 2; m > 0; m /= 2) sum += __shfl_xor_sync(group, sum, m);
+    const float r = rsqrtf(sum * (1.0f / D) + eps);
+    const Two rr = two(r, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mul(x[i], rr);
+  }
+  uint32_t y[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i0 = STYLE == 0 ? j : 2 * j, i1 = STYLE == 0 ? j + 4 : 2 * j + 1;
+    const Two o0 = STYLE == 0 ? x[i1] : swapped(x[i0]), o1 = STYLE == 0 ? x[i0] : swapped(x[i1]);
+    y[i0] = to_bf16x2(fma2(x[i0], rot.p[j][0], mul(o0, rot.p[j][1])));
+    y[i1] = to_bf16x2(fma2(x[i1], rot.p[j][2], mul(o1, rot.p[j][3])));
+  }
+  return {make_uint4(y[0], y[1], y[2], y[3]), make_uint4(y[4], y[5], y[6], y[7])};
 }
 
 // One CTA per token.  D/16 threads share a row; a thread holds the 16-byte
 // vectors c and c + D/16 of it, so that both members of a rotate-half pair
-// (i, i + D/2), and of an adjacent pair (2i, 2i + 1), are its own: no
-// exchange but the norm's sum over the row's threads.  The token's cos and
-// sin are computed once, by the first D/2 threads, while the first rows'
-// loads are in flight, and laid out so that the row's threads read 16 bytes
-// each from different banks.
+// (i, i + D/2), and of an adjacent pair (2i, 2i + 1), are its own: no exchange
+// but the norm's sum over the row's threads.  Its 8 pairs' cos and sin (times
+// the norm's weights) are the same for every row that it takes: they stay in
+// registers.  They are computed once per token by the first D/2 threads, while
+// the first rows of every role are on their way.
 constexpr int kRowThreads = 512;  // most threads of a CTA
+#ifndef V_RA
+#define V_RA 4
+#endif
+constexpr int kQueriesAhead = V_RA;
 
-template <int D, int STYLE>
+template <int D, int STYLE, bool NORM>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int TPR = D / 16;          // threads of a row
   const int NT = blockDim.x;           // a multiple of 32
   const int RPP = NT / TPR;            // rows of a pass
-  // 8 (cos, sin) pairs per thread of a row, as 4 float4: [j][c]
-  __shared__ float4 cs[4][TPR];
+  __shared__ float4 s_cs[4][TPR];      // see set_rotation; by thread of a row
   const int tid = threadIdx.x;
-  const int c = tid % TPR;
+  const int c = tid % TPR, w0 = tid / TPR;
   const int64_t t = blockIdx.x;
+  const bool append = a.slots != nullptr;
+
+  const uint16_t* q_in = a.q.data + t * a.q.ts + w0 * a.q.hs + c * 8;
+  const uint16_t* k_in = a.k.data + t * a.k.ts + w0 * a.k.hs + c * 8;
+  const uint16_t* v_in = a.v.data + t * a.v.ts + w0 * a.v.hs + c * 8;
+  const int64_t q_step = RPP * a.q.hs, k_step = RPP * a.k.hs, v_step = RPP * a.v.hs;
+  Vecs q[kQueriesAhead], k, v;
+#pragma unroll
+  for (int i = 0; i < kQueriesAhead; ++i)
+    if (w0 + i * RPP < a.nq) q[i] = load_row<D>(q_in + i * q_step);
+  if (w0 < a.nk) k = load_row<D>(k_in);
+  if (w0 < a.nv) v = load_row<D>(v_in);
   const int32_t pos = a.positions[t];
+  int64_t slot = append ? a.slots[t] : -1;
   if (pos < 0) return;
-  int64_t slot = -1;
-  if (a.slots != nullptr) {
-    slot = a.slots[t];
-    if (slot < -1 || slot >= a.num_slots) {
-      if (tid == 0) record(a.st, kErrBadBlock, t);
-      slot = -1;
-    }
-  }
-  const int64_t block = slot < 0 ? 0 : slot / a.block_size;
-  const int64_t cache_at =
-      slot < 0 ? -1 : block * a.block_stride + (slot - block * a.block_size) * a.token_stride;
-  const int rows = a.nq + a.nk + a.nv;
-
-  auto source = [&](int w) -> const uint16_t* {
-    if (w < a.nq) return a.q.data + t * a.q.ts + w * a.q.hs;
-    w -= a.nq;
-    if (w < a.nk) return a.k.data + t * a.k.ts + w * a.k.hs;
-    return a.v.data + t * a.v.ts + (w - a.nk) * a.v.hs;
-  };
-  auto target = [&](int w) -> uint16_t* {
-    if (w < a.nq) return a.q_out.data + t * a.q_out.ts + w * a.q_out.hs;
-    w -= a.nq;
-    if (w < a.nk) {
-      if (a.slots == nullptr) return a.k_out.data + t * a.k_out.ts + w * a.k_out.hs;
-      return cache_at < 0 ? nullptr : a.k_cache + cache_at + w * a.head_stride;
-    }
-    return cache_at < 0 ? nullptr : a.v_cache + cache_at + (w - a.nk) * a.head_stride;
-  };
-
-  uint4 u0, u1;
-  int w = tid / TPR;
-  if (w < rows) {
-    const uint16_t* p = source(w);
-    u0 = ld16(p + c * 8);
-    u1 = ld16(p + D / 2 + c * 8);
-  }
   for (int i = tid; i < D / 2; i += NT) {
     // Rotate-half: thread i / 8 owns pairs 8c .. 8c + 7.  Adjacent: vector c
     // holds pairs 4c .. 4c + 3 (its first four), vector c + D/16 the pairs
     // D/4 + 4c .. (its last four).
     const int owner = STYLE == 0 ? i / 8 : (i % (D / 4)) / 4;
     const int at = STYLE == 0 ? i % 8 : (i % (D / 4)) % 4 + (i >= D / 4 ? 4 : 0);
-    reinterpret_cast<float2*>(&cs[at / 2][owner])[at % 2] = cos_sin(pos, a.turns[i]);
+    const float2 v2 = cos_sin(pos, a.turns[i]);
+    float* to = reinterpret_cast<float*>(&s_cs[at / 2][owner]) + at % 2;
+    to[0] = v2.x;
+    to[2] = v2.y;
+  }
+  if (append && (slot < -1 || slot >= a.num_slots)) {
+    if (tid == 0) record(a.st, kErrBadBlock, t);
+    slot = -1;
   }
   __syncthreads();
 
-  // Whole warps stay in the loop: the norm's sum is a shuffle over the row.
-  for (int first = 0; first < rows; first += RPP) {
-    w = first + tid / TPR;
-    const bool live = w < rows;
-    if (first > 0 && live) {
-      const uint16_t* p = source(w);
-      u0 = ld16(p + c * 8);
-      u1 = ld16(p + D / 2 + c * 8);
-    }
-    uint16_t* out = live ? target(w) : nullptr;
-    if (w < a.nq + a.nk) {
-      float x[16];
-      unpack(u0, x);
-      unpack(u1, x + 8);
-      const uint16_t* weight = w < a.nq ? a.q_weight : a.k_weight;
-      // rows of a role with and without norm can meet in one warp: the sum
-      // is taken by all of them
-      float sq = 0.f;
+  Rotation rot;
+  auto set_role = [&](const uint16_t* weight) {
+    Vecs g = {make_uint4(kOnes, kOnes, kOnes, kOnes), make_uint4(kOnes, kOnes, kOnes, kOnes)};
+    if (NORM && weight != nullptr) g = load_row<D>(weight + c * 8);
+    set_rotation<STYLE>(rot, &s_cs[0][c], TPR, g);
+  };
+  set_role(a.q_weight);
+  {
+    uint16_t* out = a.q_out.data + t * a.q_out.ts + w0 * a.q_out.hs + c * 8;
+    const int64_t out_step = RPP * a.q_out.hs;
+    for (int w = w0; w < a.nq;) {  // a row's threads stay together
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sq = fmaf(x[i], x[i], sq);
-      const unsigned group = TPR == 32 ? 0xffffffffu : ((1u << TPR) - 1u) << ((tid & 31) / TPR * TPR);
-#pragma unroll
-      for (int m = TPR / 2; m > 0; m /= 2) sq += __shfl_xor_sync(group, sq, m);
-      if (weight != nullptr) {
-        const float r = rsqrtf(sq * (1.0f / D) + a.eps);
-        float g[16];
-        unpack(ld16(weight + c * 8), g);
-        unpack(ld16(weight + D / 2 + c * 8), g + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * g[i];
+      for (int i = 0; i < kQueriesAhead; ++i) {
+        if (w >= a.nq) break;
+        const Vecs y = turn_row<D, STYLE, NORM>(q[i], rot, a.q_weight != nullptr, a.eps);
+        if (w + kQueriesAhead * RPP < a.nq) q[i] = load_row<D>(q_in + (i + kQueriesAhead) * q_step);
+        store_row<D>(out, y);
+        out += out_step;
+        w += RPP;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 v = cs[j][c];
-        const float co[2] = {v.x, v.z}, si[2] = {v.y, v.w};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * j + e;
-          const int ia = STYLE == 0 ? i : 2 * i;
-          const int ib = STYLE == 0 ? i + 8 : 2 * i + 1;
-          const float xa = x[ia], xb = x[ib];
-          x[ia] = xa * co[e] - xb * si[e];
-          x[ib] = xb * co[e] + xa * si[e];
-        }
-      }
-      u0 = pack(x);
-      u1 = pack(x + 8);
+      q_in += kQueriesAhead * q_step;
     }
-    if (out != nullptr) {
-      st16(out + c * 8, u0);
-      st16(out + D / 2 + c * 8, u1);
-    }
+  }
+  uint16_t* k_out = a.k_out.data + t * a.k_out.ts;
+  int64_t out_hs = a.k_out.hs, cache_at = 0;
+  if (append) {
+    if (slot < 0) return;  // not stored
+    const int64_t block = slot / a.block_size;
+    cache_at = block * a.block_stride + (slot - block * a.block_size) * a.token_stride;
+    k_out = a.k_cache + cache_at;
+    out_hs = a.head_stride;
+  }
+  if (NORM) set_role(a.k_weight);
+  k_out += w0 * out_hs + c * 8;
+  for (int w = w0; w < a.nk; w += RPP) {
+    store_row<D>(k_out, turn_row<D, STYLE, NORM>(k, rot, a.k_weight != nullptr, a.eps));
+    k_in += k_step;
+    k_out += RPP * out_hs;
+    if (w + RPP < a.nk) k = load_row<D>(k_in);
+  }
+  uint16_t* v_out = a.v_cache + cache_at + w0 * out_hs + c * 8;
+  for (int w = w0; w < a.nv; w += RPP) {
+    store_row<D>(v_out, v);
+    v_in += v_step;
+    v_out += RPP * out_hs;
+    if (w + RPP < a.nv) v = load_row<D>(v_in);
   }
 }
 
