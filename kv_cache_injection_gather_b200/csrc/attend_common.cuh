@@ -87,7 +87,7 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
 }
 // The rest of a wait: gives up after about two seconds, or once another thread
 // has; without a flag only the limit counts.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int32_t* failed) {
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int32_t* failed) {
   const long long began = clock64();
   while (!bar_done(bar, parity)) {
     if (failed != nullptr && *failed) return false;
@@ -431,9 +431,8 @@ __device__ __forceinline__ uint32_t dims_at(int k) {
 // Warp g of W brings every W-th of the tiles K0 V0 K1 V1 ... of keys [lo, hi)
 // of request r and KV head h into a ring of NS slots of kTileKeys x D.  (A
 // tile's look-ups, waits and copies take one warp some 2000 cycles, mostly
-// latency, so whole tiles go to warps in turn.  W divides NS: a slot is always
-// the same warp's, which so sees every phase of its barriers.)  full[] and
-// empty[] take one arrival.  A tile comes as boxes, or key by key (keys outside
+// latency, so whole tiles go to warps in turn.)  full[] and empty[] take one
+// arrival.  A tile comes as boxes, or key by key (keys outside
 // [first_key, hi) as zeros) where a box holds keys of two blocks and where
 // there is no map; with ZERO_EDGE also values that run past hi.  Boxes leave
 // keys outside the range as they find them.  A block outside the cache sets
@@ -444,7 +443,12 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
                                              unsigned char* ring, uint64_t* full, uint64_t* empty,
                                              volatile int32_t* failed, int32_t* bad) {
   constexpr int CPR = D / 8, kSlotBytes = kTileKeys * D * 2;
-  static_assert(NS % W == 0, "a slot belongs to one warp");
+  // A warp may wait for tile u - NS to be read only when tile u - 2 NS has
+  // been: a parity tells neighbouring phases apart, no more.  Either the warp
+  // has waited for that one (a slot is always the same warp's), or it has seen
+  // tile u - W - NS read, a later one of the same kind, and keys are read in
+  // order, and values are.
+  static_assert(W <= NS && (NS % W == 0 || (NS - W) % 2 == 0), "phases of a slot in turn");
   const int lane = threadIdx.x & 31;
   const int32_t bits = max(0, a.box_log2), boxes = kTileKeys >> bits;
   const int32_t slab = h * a.head_slabs;
@@ -546,7 +550,7 @@ __device__ __forceinline__ void load_queries(unsigned char* tile, int rows, int 
 // tiled product came out infinite or NaN although keys that they do not see
 // may have caused it (0 * NaN).  o: dims lane, lane + 32, ...
 template <int D>
-__device__ __noinline__ void row_by_keys(const AttendArgs& a, int32_t r, int32_t h, const uint16_t* q, int32_t lo,
+__device__ __forceinline__ void row_by_keys(const AttendArgs& a, int32_t r, int32_t h, const uint16_t* q, int32_t lo,
                                          int32_t hi, float& m, float& l, float (&o)[D / 32]) {
   const int lane = threadIdx.x & 31;
   float x[D / 32];

@@ -33,8 +33,10 @@ constexpr int kUnitRows = 2 * kStreamRows;
 template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
-  static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr int kGather = D == 128 ? 5 : 4;       // gather warps
+  static constexpr int kSlots = D == 128 ? 5 : 7;
+  // 12 warps, as that leaves a thread 168 registers: a softmax thread keeps a
+  // row of 128 scores.
+  static constexpr int kGather = 3;
   static constexpr int kProductWarp = 8 + kGather;
   static constexpr int kThreads = (8 + kGather + 1) * 32;
   static constexpr int kQBytes = kUnitRows * D * 2;
@@ -43,6 +45,53 @@ struct TilesShape {
 };
 
 // ---------------------------------------------------------------- the kernel
+
+#ifndef V_POLY
+#define V_POLY 0
+#endif
+constexpr int kPolynomial = V_POLY;  // of 8 exponentials
+
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of two values up to 2^7 without the special-function unit: x = n + f with
+// n whole and |f| <= 1/2, 2^f by a polynomial of degree 4 (the coefficients
+// minimise the largest relative error on that interval, 2.6e-6 = 2^-18.5,
+// found by reweighted least squares), n added to the exponent.  Below 2^-126
+// it stays there.  Adding 1.5 * 2^23 leaves n in a sum's low bits.
+__device__ __forceinline__ Two exp2_two(Two x) {
+  const float2 in = both(x);
+  float lo, hi;  // (a NaN stays one)
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(in.x), "f"(-126.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(in.y), "f"(-126.f));
+  x = two(lo, hi);
+  const Two round = two(12582912.f, 12582912.f), back = two(-12582912.f, -12582912.f), minus = two(-1.f, -1.f);
+  const Two t = add2(x, round);
+  const Two f = fma2(add2(t, back), minus, x);
+  Two p = two(0.009570102207362652f, 0.009570102207362652f);
+  p = fma2(p, f, two(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, f, two(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, f, two(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, f, two(0.9999992847442627f, 0.9999992847442627f));
+  const float2 pf = both(p), tf = both(t);
+  return two(__uint_as_float(__float_as_uint(pf.x) + (__float_as_uint(tf.x) << 23)),
+             __uint_as_float(__float_as_uint(pf.y) + (__float_as_uint(tf.y) << 23)));
+}
 
 // The request that owns query token t: the last r with q_offsets[r] <= t.
 __device__ __forceinline__ int32_t owner_of(const AttendArgs& a, int32_t t) {
@@ -70,7 +119,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   using S = TilesShape<D>;
   constexpr int CPR = D / 8, NS = S::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2][2], bar_o;
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -128,7 +177,8 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&bar_s[i], 1);
-      bar_init(&bar_p[i], kStreamRows);
+      bar_init(&bar_p[i][0], kStreamRows);
+      bar_init(&bar_p[i][1], kStreamRows);
     }
     bar_init(&bar_q, 2 * kStreamRows);
     bar_init(&bar_o, 1);
@@ -176,15 +226,19 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       for (int32_t w = 0; w < work && ok; ++w) {
         const int st = w & 1, j = tile_of(w), slot = (2 * j + 1) % NS;
         const bool first = by_rows ? j == 0 : j < 2;
-        ok = bar_wait(&bar_p[st], (w >> 1) & 1, &s_failed);
-        wait_tile(2 * j + 1);
-        if (!ok) break;
-        tc_fence_after();
         const uint32_t va = smem_addr(ring + slot * S::kSlotBytes);
+        wait_tile(2 * j + 1);
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<D>(va + k * (D * 32), kSlabStep),
-                 product(D, false, true), !first || k > 0);
+        for (int half = 0; half < 2; ++half) {  // P comes in halves of 64 keys
+          ok = ok && bar_wait(&bar_p[st][half], (w >> 1) & 1, &s_failed);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<D>(va + k * (D * 32), kSlabStep),
+                   product(D, false, true), !first || k > 0);
+        }
+        if (!ok) break;
         if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
         if (w + 2 < work) scores(w + 2);
       }
@@ -210,27 +264,29 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       const int32_t j0 = lo + (by_rows ? w >> 1 : w) * kTileKeys;
       const bool masked = j0 + kTileKeys > lim_min;
       const int32_t seen = lim - j0;  // columns below are seen
-      uint32_t v[32];
-      float top = neg_inf();
+      uint32_t v[kTileKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld32(ts + c * 32, v);
-        tmem_wait_ld();
-        if (masked) {
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+      tmem_wait_ld();
+      if (masked) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i < seen) top = fmaxf(top, __uint_as_float(v[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-        }
+        for (int i = 0; i < kTileKeys; ++i)
+          if (i >= seen) v[i] = 0xff800000u;
       }
-      top *= a.scale_log2;  // positive: the maximum's place is the same
+      float tops[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 4]));
+#pragma unroll
+      for (int i = 8; i < kTileKeys; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e]));
+      // (the scale is positive: the maximum's place is the same)
+      const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale_log2;
       // The reference m follows the maximum only when that has risen by more
       // than 2^8: smaller steps leave P below 2^8 and O as it is.  All rows
       // of a warp take part in a correction (factor 1 where none is needed).
       float shrink = 1.f;
-      if (top > m + 8.f || (m == neg_inf() && top > m)) {
+      if (top > m + 8.f) {  // (-inf + 8 is -inf: the first seen key counts)
         shrink = exp2_fast(m - top);
         m = top;
       }
@@ -238,41 +294,54 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       // barrier's arrival followed them
       if (w >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
         l *= shrink;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          tmem_ld32(to + c * 32, v);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld<16>(to + c * 16, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * shrink);
-          tmem_st32(to + c * 32, v);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+          tmem_st<16>(to + c * 16, o);
         }
       }
       const float ref = m == neg_inf() ? 0.f : m;
-      float sum[2] = {0.f, 0.f};
+      const Two scale2 = two(a.scale_log2, a.scale_log2), ref2 = two(-ref, -ref);
+      Two sum2 = 0;
+      // P, two keys at a time, over the scores (which are all read).  A share
+      // of the exponentials is computed on the multiply-add units, as the
+      // special-function unit's 16 a cycle are what a tile waits for; where
+      // keys are masked none are (a masked key has to be 0 exactly).
+      auto probabilities = [&](auto plain) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld32(ts + c * 32, v);
-        tmem_wait_ld();
-        if (masked) {
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i >= seen) v[i] = 0xff800000u;
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int at = c * 32 + 2 * i;
+              const Two x = fma2(two(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), scale2, ref2);
+              Two e;
+              if (!decltype(plain)::value && i % 8 < kPolynomial) {
+                e = exp2_two(x);
+              } else {
+                const float2 f = both(x);
+                e = two(exp2_fast(f.x), exp2_fast(f.y));
+              }
+              sum2 = add2(sum2, e);
+              p[i] = to_bf16x2(e);
+            }
+            tmem_st16(ts + c * 16, p);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          bar_arrive(&bar_p[st][half]);
         }
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p0 = exp2_fast(fmaf(__uint_as_float(v[2 * i]), a.scale_log2, -ref));
-          const float p1 = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), a.scale_log2, -ref));
-          sum[0] += p0;
-          sum[1] += p1;
-          p[i] = to_bf16x2(p0, p1);
-        }
-        tmem_st16(ts + c * 16, p);  // over scores that have been read
-      }
-      l += sum[0] + sum[1];
-      tmem_wait_st();
-      tc_fence_before();
-      bar_arrive(&bar_p[st]);
+      };
+      if (masked) probabilities(Yes());
+      else probabilities(No());
+      const float2 sums = both(sum2);
+      l += sums.x + sums.y;
     }
   }
 
