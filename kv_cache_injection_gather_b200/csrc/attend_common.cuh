@@ -437,10 +437,10 @@ __device__ __forceinline__ uint32_t dims_at(int k) {
 // there is no map; with ZERO_EDGE also values that run past hi.  Boxes leave
 // keys outside the range as they find them.  A block outside the cache sets
 // *bad, and its keys mean nothing.
-template <int D, int NS, int W, bool ZERO_EDGE>
+template <int D, int NS, int W>
 __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map,
                                              int g, int32_t r, int32_t h, int32_t lo, int32_t hi, int32_t tiles,
-                                             unsigned char* ring, uint64_t* full, uint64_t* empty,
+                                             unsigned char* ring, uint64_t* full, uint64_t* empty, uint64_t* edge,
                                              volatile int32_t* failed, int32_t* bad) {
   constexpr int CPR = D / 8, kSlotBytes = kTileKeys * D * 2;
   // A warp may wait for tile u - NS to be read only when tile u - 2 NS has
@@ -452,9 +452,9 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
   const int lane = threadIdx.x & 31;
   const int32_t bits = max(0, a.box_log2), boxes = kTileKeys >> bits;
   const int32_t slab = h * a.head_slabs;
-  auto by_box = [&](int32_t j0, bool v) {
+  auto by_box = [&](int32_t j0) {
     const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys && (a.table_shared & ((1 << bits) - 1)) != 0;
-    return a.box_log2 >= 0 && !torn && !(ZERO_EDGE && v && hi - j0 < kTileKeys);
+    return a.box_log2 >= 0 && !torn;
   };
   // Lane i looks up box i of this warp's next tile (position -1: none), a tile
   // ahead of the copies that need it.
@@ -480,7 +480,7 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
     const int slot = u % NS;
     const uint32_t dst = smem_addr(ring + slot * kSlotBytes);
     const int32_t pos = next_pos, entry = next_entry, group = next_token >> 3;
-    const bool boxed = by_box(j0, v), fine = entry >= 0 && entry < a.num_blocks;
+    const bool boxed = by_box(j0), fine = entry >= 0 && entry < a.num_blocks;
     const uint32_t good = __ballot_sync(0xffffffffu, pos >= 0 && fine);
     if (pos >= 0 && !fine && boxed) {
       record(a.st, kErrBadBlock, pos < a.table_shared ? -1 : r);
@@ -490,7 +490,9 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
     // the whole warp goes on or stops
     if (u >= NS && !__all_sync(0xffffffffu, bar_wait(&empty[slot], ((u / NS) - 1) & 1, failed))) break;
     if (boxed) {
-      if (elect_one()) bar_expect(&full[slot], (uint32_t(__popc(good)) << bits) * (D * 2));
+      const bool clear = edge != nullptr && v && hi - j0 < kTileKeys;  // the last tile
+      uint64_t* landed = clear ? edge : &full[slot];
+      if (elect_one()) bar_expect(landed, (uint32_t(__popc(good)) << bits) * (D * 2));
       for (int box = 0; box < boxes; box += 8) {
         int32_t at_block[8], at_group[8];
 #pragma unroll
@@ -502,8 +504,16 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if ((good >> (box + i)) & 1u)
-              copy_box(dst + ((box + i) << bits) * (D * 2), map, slab, at_group[i], at_block[i], &full[slot]);
+              copy_box(dst + ((box + i) << bits) * (D * 2), map, slab, at_group[i], at_block[i], landed);
         }
+      }
+      if (clear) {
+        if (!__all_sync(0xffffffffu, bar_wait(edge, 0, failed))) break;
+        for (int i = (hi - j0) * CPR + lane; i < kTileKeys * CPR; i += 32)
+          *reinterpret_cast<uint4*>(ring + slot * kSlotBytes + tile_at<D>(i / CPR, i % CPR)) = make_uint4(0, 0, 0, 0);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&full[slot]);
       }
     } else {
       for (int first = 0; first < kTileKeys; first += 32) {

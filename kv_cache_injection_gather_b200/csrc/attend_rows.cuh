@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   const uint32_t tmem_o = tmem + 2 * NR;      // O^T, NR columns per 128 dims
 
   if (warp >= 4 && warp < S::kProductWarp) {
-    gather_tiles<D, NS, S::kGather, false>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
-                               &s_bad);
+    gather_tiles<D, NS, S::kGather>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, nullptr,
+                                    &s_failed, &s_bad);
   } else if (warp == S::kProductWarp) {
     // ---------------- products
     if (tiles > 0 && elect_one()) {

@@ -33,12 +33,13 @@ constexpr int kUnitRows = 2 * kStreamRows;
 template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
-  static constexpr int kSlots = D == 128 ? 5 : 7;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
   // 12 warps, as that leaves a thread 168 registers: a softmax thread keeps a
-  // row of 128 scores.
-  static constexpr int kGather = 3;
-  static constexpr int kProductWarp = 8 + kGather;
-  static constexpr int kThreads = (8 + kGather + 1) * 32;
+  // row of 128 scores.  One warp a stream issues its products: a wait costs a
+  // lone thread some 200 cycles of latency, and a tile has four.
+  static constexpr int kGather = 2;
+  static constexpr int kProductWarp = 8 + kGather;       // and the next
+  static constexpr int kThreads = (8 + kGather + 2) * 32;
   static constexpr int kQBytes = kUnitRows * D * 2;
   // data, and up to 1 KB to align it
   static constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
@@ -46,8 +47,11 @@ struct TilesShape {
 
 // ---------------------------------------------------------------- the kernel
 
+#ifndef V_OFF
+#define V_OFF 1
+#endif
 #ifndef V_POLY
-#define V_POLY 0
+#define V_POLY 2
 #endif
 constexpr int kPolynomial = V_POLY;  // of 8 exponentials
 
@@ -108,6 +112,20 @@ __device__ __forceinline__ int32_t owner_of(const AttendArgs& a, int32_t t) {
   return at;
 }
 
+// Token (of the request) and head (of the KV head's) of rows in steps.
+struct RowWalk {
+  int32_t token, g;
+  __device__ __forceinline__ RowWalk(const AttendArgs& a, int32_t row) : token(row / a.group), g(row % a.group) {}
+  __device__ __forceinline__ void step(const AttendArgs& a, int rows) {
+    token += rows / a.group;  // (rows is a constant and so are the quotients, for a launch)
+    g += rows % a.group;
+    if (g >= a.group) {
+      g -= a.group;
+      ++token;
+    }
+  }
+};
+
 // SHARED: the units are 256 rows of all requests' query tokens, and their keys
 // those of the shared prefix; otherwise rows and keys of one request.  Where
 // a.part_o is set, split s of a unit's keys goes to part s of the work space;
@@ -119,9 +137,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   using S = TilesShape<D>;
   constexpr int CPR = D / 8, NS = S::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2][2], bar_o;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2][2], bar_o[2], bar_edge;
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
+  __shared__ uint8_t s_odd[kUnitRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
   let_next_start();
@@ -129,7 +148,8 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   // the grid that follows does)
   const int32_t split = int32_t(blockIdx.x % a.splits);
   const int32_t h = int32_t(blockIdx.x / a.splits) % a.kv_heads;
-  const int32_t unit = int32_t(blockIdx.x / a.splits) / a.kv_heads;
+  // (the last units first: with a causal mask they see the most keys)
+  const int32_t unit = int32_t(a.units) - 1 - int32_t(blockIdx.x / a.splits) / a.kv_heads;
   int32_t r, tile;
   Request rq;
   if constexpr (SHARED) {
@@ -165,7 +185,9 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   const int32_t hi = last == all_tiles ? all : int32_t(last) * kTileKeys;
   const int32_t tiles = hi > lo ? (hi - lo + kTileKeys - 1) / kTileKeys : 0;
   const bool by_rows = rows > kStreamRows;
-  const int32_t work = by_rows ? 2 * tiles : tiles;  // products S, streams in turn
+  // tiles of a stream: all of them, or every other
+  auto tiles_of = [&](int st) { return by_rows ? tiles : (tiles - st + 1) / 2; };
+  auto first_key_of = [&](int st, int32_t i) { return lo + (by_rows ? i : 2 * i + st) * kTileKeys; };
 
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* ring = smem + S::kQBytes;
@@ -173,15 +195,16 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       bar_init(&bar_full[i], 1);
-      bar_init(&bar_empty[i], 1);
+      bar_init(&bar_empty[i], by_rows ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&bar_s[i], 1);
       bar_init(&bar_p[i][0], kStreamRows);
       bar_init(&bar_p[i][1], kStreamRows);
+      bar_init(&bar_o[i], 1);
     }
     bar_init(&bar_q, 2 * kStreamRows);
-    bar_init(&bar_o, 1);
+    bar_init(&bar_edge, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_failed = 0;
     s_bad = 0;
@@ -193,75 +216,103 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   const uint32_t tmem = s_tmem;  // S0 | S1 (128 columns each) | O0 | O1 (D each)
   const uint32_t tmem_o = tmem + 256;
   constexpr int OC = 128;        // columns between O0 and O1
+  constexpr int kRowStep = 2 * kStreamRows / CPR;  // rows that the softmax warps move at a time
 
   float m = neg_inf(), l = 0.f;  // softmax warps: of this thread's row
   int32_t lim = 0;
 
   if (warp >= 8 && warp < S::kProductWarp) {
-    gather_tiles<D, NS, S::kGather, true>(a, &k_map, &v_map, warp - 8, r, h, lo, hi, tiles, ring, bar_full, bar_empty, &s_failed,
-                              &s_bad);
-  } else if (warp == S::kProductWarp) {
-    // ---------------- products
-    if (elect_one()) {
-      bool ok = true;
-      auto tile_of = [&](int32_t w) { return by_rows ? w >> 1 : w; };
-      auto wait_tile = [&](int32_t u) { ok = ok && bar_wait(&bar_full[u % NS], (u / NS) & 1, &s_failed); };
-      auto scores = [&](int32_t w) {
-        const int st = w & 1, j = tile_of(w), slot = (2 * j) % NS;
-        wait_tile(2 * j);
-        if (!ok) return;
+    gather_tiles<D, NS, S::kGather>(a, &k_map, &v_map, warp - 8, r, h, lo, hi, tiles, ring, bar_full, bar_empty,
+                                    &bar_edge, &s_failed, &s_bad);
+  } else if (warp >= S::kProductWarp) {
+    // ---------------- products of stream st
+    const int st = warp - S::kProductWarp;
+    const int32_t n = tiles_of(st);
+    if (n > 0 && elect_one()) {
+      const uint32_t ts = tmem + st * 128, to = tmem_o + st * OC;
+      const uint32_t qa = smem_addr(smem) + (by_rows ? st * S::kSlotBytes : 0), ring_at = smem_addr(ring);
+      const int step = by_rows ? 2 : 4;  // slots from a tile to the next; its values are in the next slot
+      int slot = by_rows ? 0 : 2 * st, next = slot;
+      uint32_t parity = 0, next_parity = 0;
+      auto advance = [&] {
+        next = slot + step;
+        next_parity = parity;
+        if (next >= NS) {
+          next -= NS;
+          next_parity ^= 1;
+        }
+      };
+      auto scores = [&](int at) {
         tc_fence_after();
-        const uint32_t qa = smem_addr(smem) + (by_rows ? st * S::kSlotBytes : 0);
-        const uint32_t ka = smem_addr(ring + slot * S::kSlotBytes);
+        const uint32_t ka = ring_at + at * S::kSlotBytes;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + st * 128, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
+          mma_ss(ts, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
                  product(kTileKeys, false, false), k > 0);
         tc_commit(&bar_s[st]);
-        if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
+        tc_commit(&bar_empty[at]);
       };
-      if (work > 0) ok = bar_wait(&bar_q, 0, &s_failed);
-      if (work > 0) scores(0);
-      if (work > 1) scores(1);
-      for (int32_t w = 0; w < work && ok; ++w) {
-        const int st = w & 1, j = tile_of(w), slot = (2 * j + 1) % NS;
-        const bool first = by_rows ? j == 0 : j < 2;
-        const uint32_t va = smem_addr(ring + slot * S::kSlotBytes);
-        wait_tile(2 * j + 1);
+      bool ok = bar_wait(&bar_q, 0, &s_failed) && bar_wait(&bar_full[slot], parity, &s_failed);
+      // the second stream starts half a turn late, so that one's softmax runs
+      // beside the other's products
+      if (st == 1) ok = ok && bar_wait(&bar_p[0][V_OFF], 0, &s_failed);
+      if (ok) scores(slot);
+      for (int32_t i = 0; i < n && ok; ++i) {
+        advance();
+        const bool more = i + 1 < n;
+        // both tiles before the probabilities, which come last
+        ok = bar_wait(&bar_full[slot + 1], parity, &s_failed) &&
+             (!more || bar_wait(&bar_full[next], next_parity, &s_failed));
+        const uint32_t va = ring_at + (slot + 1) * S::kSlotBytes;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // P comes in halves of 64 keys
-          ok = ok && bar_wait(&bar_p[st][half], (w >> 1) & 1, &s_failed);
+          ok = ok && bar_wait(&bar_p[st][half], i & 1, &s_failed);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int k = 4 * half; k < 4 * half + 4; ++k)
-            mma_ts(tmem_o + st * OC, tmem + st * 128 + k * 8, operand<D>(va + k * (D * 32), kSlabStep),
-                   product(D, false, true), !first || k > 0);
+            mma_ts(to, ts + k * 8, operand<D>(va + k * (D * 32), kSlabStep), product(D, false, true), i > 0 || k > 0);
         }
         if (!ok) break;
-        if (!by_rows || st == 1) tc_commit(&bar_empty[slot]);
-        if (w + 2 < work) scores(w + 2);
+        tc_commit(&bar_empty[slot + 1]);
+        // (the next scores overwrite the probabilities that these products
+        // read: products run in the order of their issue)
+        if (more) scores(next);
+        slot = next;
+        parity = next_parity;
       }
-      tc_commit(&bar_o);
-      bar_wait(&bar_o, 0, nullptr);  // nothing in flight beyond this point
+      tc_commit(&bar_o[st]);
+      bar_wait(&bar_o[st], 0, nullptr);  // nothing in flight beyond this point
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // ---------------- softmax of stream st, one row a thread
-    load_queries<D>(smem, rows, by_rows ? kUnitRows : kStreamRows, tid, 2 * kStreamRows, a.q.data, [&](int row) {
-      return a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs;
-    });
-    bar_arrive(&bar_q);
+    {
+      RowWalk at(a, row0 + tid / CPR);
+      const int c = tid % CPR;
+      for (int row = tid / CPR; row < (by_rows ? kUnitRows : kStreamRows); row += kRowStep) {
+        const bool live = row < rows;
+        const uint16_t* src = a.q.data;
+        if (live) src += int64_t(rq.tok0 + at.token) * a.q.ts + (h * a.group + at.g) * a.q.hs + c * 8;
+        cp_async16(smem_addr(smem + tile_at<D>(row, c)), src, live ? 16 : 0);
+        at.step(a, kRowStep);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      proxy_fence();
+      bar_arrive(&bar_q);
+    }
     const int st = warp / 4, row = (tid & 127) + (by_rows ? st * kStreamRows : 0);
     lim = row < rows ? min(hi, limit_of(row)) : hi;
     const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes a warp
     const uint32_t ts = tmem + st * 128 + lanes, to = tmem_o + st * OC + lanes;
-    for (int32_t w = st; w < work; w += 2) {
+    const int32_t n = tiles_of(st);
+    for (int32_t it = 0; it < n; ++it) {
       // the whole warp goes on or stops: what follows is warp-wide
-      if (!__all_sync(0xffffffffu, bar_wait(&bar_s[st], (w >> 1) & 1, &s_failed))) break;
+      if (!__all_sync(0xffffffffu, bar_wait(&bar_s[st], it & 1, &s_failed))) break;
       tc_fence_after();
-      const int32_t j0 = lo + (by_rows ? w >> 1 : w) * kTileKeys;
+      const int32_t j0 = first_key_of(st, it);
       const bool masked = j0 + kTileKeys > lim_min;
       const int32_t seen = lim - j0;  // columns below are seen
       uint32_t v[kTileKeys];
@@ -292,7 +343,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       }
       // the products with V up to this stream's previous tile are done: the
       // barrier's arrival followed them
-      if (w >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
+      if (it > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
         l *= shrink;
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -358,7 +409,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     // joined sums of a row that both streams worked on: stream 1 hands its
     // part over through the ring
     float* part = reinterpret_cast<float*>(ring);  // [dim][row]
-    float* s_m = reinterpret_cast<float*>(smem);   // over the queries
+    float* s_m = part + D * kStreamRows;
     float* s_l = s_m + kStreamRows;
     float w0 = 1.f, w1 = 0.f;
     const bool two = !by_rows && tiles > 1;
@@ -392,60 +443,46 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       const int32_t head = head_of(mine ? row : 0);
       const bool none = l == 0.f || tiles == 0;
       const float inv = none ? 0.f : 1.f / l;
-      uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
       const int64_t part_row = (int64_t(split) * a.num_tokens + t) * a.num_heads + head;
       const bool to_part = a.part_o != nullptr;
-      // A row is odd if keys past its limit, or a bad block, were among its
-      // tiles and its sums are not finite (or the block was bad): 0 * NaN.
-      const bool suspect = lim < hi || s_bad != 0;
-      bool odd = s_bad != 0;
-      if (tiles > 0) {
-        if (__any_sync(0xffffffffu, suspect && mine)) {
-          bool fine = finite(l);
+      // A row is odd if keys past its limit were among its tiles and its sums
+      // are not finite (0 * NaN), or if a block was bad.
+      bool fine = finite(l);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(to + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float x = __uint_as_float(v[i]) * w0;
-              if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
-              fine = fine && finite(x);
-            }
-          }
-          odd = odd || (suspect && !fine);
-        }
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        if (tiles > 0) {
           tmem_ld32(to + c * 32, v);
           tmem_wait_ld();
+        }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x = __uint_as_float(v[i]) * w0;
-            if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
-            v[i] = __float_as_uint(to_part ? x : none ? 0.f : x * inv);
-          }
-          if (mine && !odd && to_part) {
+        for (int i = 0; i < 32; ++i) {
+          float x = tiles > 0 ? __uint_as_float(v[i]) * w0 : 0.f;
+          if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
+          fine = fine && finite(x);
+          v[i] = __float_as_uint(to_part ? x : none ? 0.f : x * inv);
+        }
+        if (to_part) {
+          if (mine && tiles > 0) {
             float* dst = a.part_o + part_row * D + c * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else if (mine && !odd) {
+          }
+        } else {  // over the queries, for stores of whole rows
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[e] = to_bf16x2(__uint_as_float(v[i * 8 + 2 * e]), __uint_as_float(v[i * 8 + 2 * e + 1]));
-              st16(out + c * 32 + i * 8, make_uint4(o[0], o[1], o[2], o[3]));
-            }
+            for (int e = 0; e < 4; ++e)
+              o[e] = to_bf16x2(__uint_as_float(v[i * 8 + 2 * e]), __uint_as_float(v[i * 8 + 2 * e + 1]));
+            *reinterpret_cast<uint4*>(smem + row * (D * 2) + (((c * 4 + i) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-      } else if (mine && !to_part) {
-        for (int i = 0; i < CPR; ++i) st16(out + i * 8, make_uint4(0, 0, 0, 0));
       }
+      const bool odd = tiles > 0 && (s_bad != 0 || (lim < hi && !fine));
+      s_odd[row] = odd;
       if (mine && !odd && to_part)
         a.part_ml[part_row] = make_float2(m, l);
       else if (mine && !odd && a.lse != nullptr)
@@ -481,6 +518,16 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   if (warp == S::kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
+  }
+  if (!failed && warp < 8 && a.part_o == nullptr) {
+    RowWalk at(a, row0 + tid / CPR);
+    const int c = tid % CPR;
+    for (int row = tid / CPR; row < rows; row += kRowStep) {
+      if (!s_odd[row])
+        st16(a.out.data + int64_t(rq.tok0 + at.token) * a.out.ts + (h * a.group + at.g) * a.out.hs + c * 8,
+             *reinterpret_cast<const uint4*>(smem + row * (D * 2) + ((c ^ (row & 7)) << 4)));
+      at.step(a, kRowStep);
+    }
   }
 }
 

@@ -452,6 +452,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   if (p.parts) {
     isq::AttendArgs sa = a;
     sa.splits = p.parts;
+    sa.units = p.shared_units;
     sa.part_ml = a.part_ml = static_cast<float2*>(workspace);
     sa.part_o = a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
     const AttendKernel k = attend_tiles_of(query->head_dim, true);
