@@ -556,19 +556,21 @@ __device__ __forceinline__ void load_queries(unsigned char* tile, int rows, int 
   proxy_fence();
 }
 
-// One row over keys [lo, hi) by a warp, key after key in fp32: for rows whose
-// tiled product came out infinite or NaN although keys that they do not see
-// may have caused it (0 * NaN).  o: dims lane, lane + 32, ...
+// One row (of a tile of queries in shared memory) over keys [lo, hi) by a
+// warp, key after key in fp32: for rows whose tiled product came out infinite
+// or NaN although keys that they do not see may have caused it (0 * NaN).  o:
+// dims lane, lane + 32, ...
 template <int D>
-__device__ __forceinline__ void row_by_keys(const AttendArgs& a, int32_t r, int32_t h, const uint16_t* q, int32_t lo,
-                                         int32_t hi, float& m, float& l, float (&o)[D / 32]) {
+__device__ __forceinline__ void row_by_keys(const AttendArgs& a, int32_t r, int32_t h, const unsigned char* q_tile,
+                                            int row, int32_t lo, int32_t hi, float& m, float& l, float (&o)[D / 32]) {
   const int lane = threadIdx.x & 31;
   float x[D / 32];
   m = neg_inf();
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    x[i] = __uint_as_float(uint32_t(q[lane + 32 * i]) << 16);
+    const int d = lane + 32 * i;
+    x[i] = lo_f(*reinterpret_cast<const uint16_t*>(q_tile + tile_at<D>(row, d >> 3) + (d & 7) * 2));
     o[i] = 0.f;
   }
   for (int32_t j = lo; j < hi; ++j) {
@@ -577,7 +579,7 @@ __device__ __forceinline__ void row_by_keys(const AttendArgs& a, int32_t r, int3
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      s = fmaf(x[i], __uint_as_float(uint32_t(a.k_cache[at + lane + 32 * i]) << 16), s);
+      s = fmaf(x[i], lo_f(a.k_cache[at + lane + 32 * i]), s);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
     s *= a.scale_log2;
@@ -588,7 +590,7 @@ __device__ __forceinline__ void row_by_keys(const AttendArgs& a, int32_t r, int3
     l = l * shrink + p;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      o[i] = o[i] * shrink + p * __uint_as_float(uint32_t(a.v_cache[at + lane + 32 * i]) << 16);
+      o[i] = o[i] * shrink + p * lo_f(a.v_cache[at + lane + 32 * i]);
   }
 }
 

@@ -383,8 +383,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   for (int row = warp; row < rows; row += NT / 32) {
     if (!s_odd[row]) continue;
     float m, l, x[D / 32];
-    row_by_keys<D>(a, r, h, a.q.data + int64_t(rq.tok0 + token_of(row)) * a.q.ts + head_of(row) * a.q.hs,
-                   max(lo, a.first_key), s_lim[row], m, l, x);
+    row_by_keys<D>(a, r, h, q_tile, row, max(lo, a.first_key), s_lim[row], m, l, x);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) st_cluster(join_at(row, lane + 32 * i), x[i]);
     if (lane < a.splits) join_ml(row, m, l, lane);

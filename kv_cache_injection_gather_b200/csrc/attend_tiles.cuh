@@ -47,11 +47,8 @@ struct TilesShape {
 
 // ---------------------------------------------------------------- the kernel
 
-#ifndef V_OFF
-#define V_OFF 1
-#endif
 #ifndef V_POLY
-#define V_POLY 2
+#define V_POLY 1
 #endif
 constexpr int kPolynomial = V_POLY;  // of 8 exponentials
 
@@ -115,12 +112,15 @@ __device__ __forceinline__ int32_t owner_of(const AttendArgs& a, int32_t t) {
 // Token (of the request) and head (of the KV head's) of rows in steps.
 struct RowWalk {
   int32_t token, g;
-  __device__ __forceinline__ RowWalk(const AttendArgs& a, int32_t row) : token(row / a.group), g(row % a.group) {}
-  __device__ __forceinline__ void step(const AttendArgs& a, int rows) {
-    token += rows / a.group;  // (rows is a constant and so are the quotients, for a launch)
-    g += rows % a.group;
-    if (g >= a.group) {
-      g -= a.group;
+  int32_t group, step_token, step_g;
+  __device__ __forceinline__ RowWalk(int32_t group_, int32_t row, int32_t step)
+      : token(row / group_), g(row - token * group_), group(group_), step_token(step / group_),
+        step_g(step - step_token * group_) {}
+  __device__ __forceinline__ void step() {
+    token += step_token;
+    g += step_g;
+    if (g >= group) {
+      g -= group;
       ++token;
     }
   }
@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2][2], bar_o[2], bar_edge;
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
-  __shared__ uint8_t s_odd[kUnitRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
   let_next_start();
@@ -150,6 +149,29 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   const int32_t h = int32_t(blockIdx.x / a.splits) % a.kv_heads;
   // (the last units first: with a causal mask they see the most keys)
   const int32_t unit = int32_t(a.units) - 1 - int32_t(blockIdx.x / a.splits) / a.kv_heads;
+  if (!SHARED && blockIdx.x == gridDim.x - 1) {
+    check_requests<S::kThreads>(a);
+    return;
+  }
+  // what needs no metadata first, beside the loads of find_unit
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      bar_init(&bar_full[i], 1);
+      bar_init(&bar_empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bar_s[i], 1);
+      bar_init(&bar_p[i][0], kStreamRows);
+      bar_init(&bar_p[i][1], kStreamRows);
+      bar_init(&bar_o[i], 1);
+    }
+    bar_init(&bar_q, 2 * kStreamRows);
+    bar_init(&bar_edge, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_failed = 0;
+    s_bad = 0;
+  }
+  if (warp == S::kProductWarp) tmem_alloc(&s_tmem, 512);
   int32_t r, tile;
   Request rq;
   if constexpr (SHARED) {
@@ -157,12 +179,11 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     tile = unit;
     rq = {0, a.num_tokens, 0, 0};
   } else {
-    if (blockIdx.x == gridDim.x - 1) {
-      check_requests<S::kThreads>(a);
+    find_unit<kUnitRows, S::kThreads>(a, unit, r, tile, rq);
+    if (r < 0) {
+      if (warp == S::kProductWarp) tmem_free(s_tmem, 512);
       return;
     }
-    find_unit<kUnitRows, S::kThreads>(a, unit, r, tile, rq);
-    if (r < 0) return;
   }
 
   const int32_t row0 = tile * kUnitRows;
@@ -192,24 +213,6 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* ring = smem + S::kQBytes;
 
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], 1);
-      bar_init(&bar_empty[i], by_rows ? 2 : 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bar_s[i], 1);
-      bar_init(&bar_p[i][0], kStreamRows);
-      bar_init(&bar_p[i][1], kStreamRows);
-      bar_init(&bar_o[i], 1);
-    }
-    bar_init(&bar_q, 2 * kStreamRows);
-    bar_init(&bar_edge, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_failed = 0;
-    s_bad = 0;
-  }
-  if (warp == S::kProductWarp) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -242,6 +245,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
           next_parity ^= 1;
         }
       };
+      auto free_slot = [&](int at) {  // two arrivals: both streams', or the one's that reads the tile
+        tc_commit(&bar_empty[at]);
+        if (!by_rows) tc_commit(&bar_empty[at]);
+      };
       auto scores = [&](int at) {
         tc_fence_after();
         const uint32_t ka = ring_at + at * S::kSlotBytes;
@@ -250,12 +257,12 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
           mma_ss(ts, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
                  product(kTileKeys, false, false), k > 0);
         tc_commit(&bar_s[st]);
-        tc_commit(&bar_empty[at]);
+        free_slot(at);
       };
       bool ok = bar_wait(&bar_q, 0, &s_failed) && bar_wait(&bar_full[slot], parity, &s_failed);
       // the second stream starts half a turn late, so that one's softmax runs
       // beside the other's products
-      if (st == 1) ok = ok && bar_wait(&bar_p[0][V_OFF], 0, &s_failed);
+      if (st == 1) ok = ok && bar_wait(&bar_p[0][1], 0, &s_failed);
       if (ok) scores(slot);
       for (int32_t i = 0; i < n && ok; ++i) {
         advance();
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
             mma_ts(to, ts + k * 8, operand<D>(va + k * (D * 32), kSlabStep), product(D, false, true), i > 0 || k > 0);
         }
         if (!ok) break;
-        tc_commit(&bar_empty[slot + 1]);
+        free_slot(slot + 1);
         // (the next scores overwrite the probabilities that these products
         // read: products run in the order of their issue)
         if (more) scores(next);
@@ -288,14 +295,14 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   } else {
     // ---------------- softmax of stream st, one row a thread
     {
-      RowWalk at(a, row0 + tid / CPR);
+      RowWalk at(a.group, row0 + tid / CPR, kRowStep);
       const int c = tid % CPR;
       for (int row = tid / CPR; row < (by_rows ? kUnitRows : kStreamRows); row += kRowStep) {
         const bool live = row < rows;
         const uint16_t* src = a.q.data;
         if (live) src += int64_t(rq.tok0 + at.token) * a.q.ts + (h * a.group + at.g) * a.q.hs + c * 8;
         cp_async16(smem_addr(smem + tile_at<D>(row, c)), src, live ? 16 : 0);
-        at.step(a, kRowStep);
+        at.step();
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -445,47 +452,54 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       const float inv = none ? 0.f : 1.f / l;
       const int64_t part_row = (int64_t(split) * a.num_tokens + t) * a.num_heads + head;
       const bool to_part = a.part_o != nullptr;
+      uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
+      const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;  // for 32-byte stores
       // A row is odd if keys past its limit were among its tiles and its sums
       // are not finite (0 * NaN), or if a block was bad.
-      bool fine = finite(l);
+      float check = l * 0.f;  // NaN once a sum is not finite
+      const float scale = to_part ? w0 : w0 * inv, scale1 = to_part ? w1 : w1 * inv;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
+      for (int c = 0; c < D / 16; ++c) {
+        float x[16];
         if (tiles > 0) {
-          tmem_ld32(to + c * 32, v);
+          tmem_ld<16>(to + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&x));
           tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        }
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(part[(c * 16 + i) * kStreamRows + rr], scale1, x[i] * scale);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= scale;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x = tiles > 0 ? __uint_as_float(v[i]) * w0 : 0.f;
-          if (two) x = fmaf(part[(c * 32 + i) * kStreamRows + rr], w1, x);
-          fine = fine && finite(x);
-          v[i] = __float_as_uint(to_part ? x : none ? 0.f : x * inv);
-        }
+        for (int i = 0; i < 16; ++i) check = fmaf(x[i], 0.f, check);
+        if (!mine) continue;
         if (to_part) {
-          if (mine && tiles > 0) {
-            float* dst = a.part_o + part_row * D + c * 32;
+          float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * D + c * 16);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        } else {  // over the queries, for stores of whole rows
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else {
+          uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = to_bf16x2(__uint_as_float(v[i * 8 + 2 * e]), __uint_as_float(v[i * 8 + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(smem + row * (D * 2) + (((c * 4 + i) ^ (row & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+          for (int i = 0; i < 8; ++i) o[i] = none ? 0u : to_bf16x2(x[2 * i], x[2 * i + 1]);
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c * 16), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
+          } else {
+            st16(out + c * 16, make_uint4(o[0], o[1], o[2], o[3]));
+            st16(out + c * 16 + 8, make_uint4(o[4], o[5], o[6], o[7]));
           }
         }
       }
-      const bool odd = tiles > 0 && (s_bad != 0 || (lim < hi && !fine));
-      s_odd[row] = odd;
-      if (mine && !odd && to_part)
+      const bool odd = tiles > 0 && (s_bad != 0 || (lim < hi && check != 0.f));
+      if (mine && to_part)
         a.part_ml[part_row] = make_float2(m, l);
-      else if (mine && !odd && a.lse != nullptr)
+      else if (mine && a.lse != nullptr)
         a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
       // odd rows, one after the other by the whole warp
       uint32_t todo = __ballot_sync(0xffffffffu, odd && mine);
@@ -494,8 +508,9 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         todo &= todo - 1;
         const int64_t tt = __shfl_sync(0xffffffffu, t, from);
         const int32_t hh = __shfl_sync(0xffffffffu, head, from), top = __shfl_sync(0xffffffffu, lim, from);
+        const int odd_row = __shfl_sync(0xffffffffu, row, from);
         float om, ol, o[D / 32];
-        row_by_keys<D>(a, r, h, a.q.data + tt * a.q.ts + hh * a.q.hs, lo, top, om, ol, o);
+        row_by_keys<D>(a, r, h, smem, odd_row, lo, top, om, ol, o);
         if (to_part) {
           const int64_t at = (int64_t(split) * a.num_tokens + tt) * a.num_heads + hh;
 #pragma unroll
@@ -518,16 +533,6 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   if (warp == S::kProductWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
-  }
-  if (!failed && warp < 8 && a.part_o == nullptr) {
-    RowWalk at(a, row0 + tid / CPR);
-    const int c = tid % CPR;
-    for (int row = tid / CPR; row < rows; row += kRowStep) {
-      if (!s_odd[row])
-        st16(a.out.data + int64_t(rq.tok0 + at.token) * a.out.ts + (h * a.group + at.g) * a.out.hs + c * 8,
-             *reinterpret_cast<const uint4*>(smem + row * (D * 2) + ((c ^ (row & 7)) << 4)));
-      at.step(a, kRowStep);
-    }
   }
 }
 
