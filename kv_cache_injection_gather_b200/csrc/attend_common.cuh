@@ -451,6 +451,7 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
   static_assert(W <= NS && (NS % W == 0 || (NS - W) % 2 == 0), "phases of a slot in turn");
   const int lane = threadIdx.x & 31;
   const int32_t bits = max(0, a.box_log2), boxes = kTileKeys >> bits;
+  const bool whole = a.block_size == 1 << bits;  // a box is a block
   const int32_t slab = h * a.head_slabs;
   auto by_box = [&](int32_t j0) {
     const bool torn = j0 < a.table_shared && a.table_shared - j0 < kTileKeys && (a.table_shared & ((1 << bits) - 1)) != 0;
@@ -462,8 +463,8 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
   auto look_up = [&](int32_t t) {
     const int32_t j0 = lo + t * kTileKeys, key = lane << bits;
     next_pos = a.box_log2 >= 0 && t < tiles && lane < boxes && hi - j0 > key ? j0 + key : -1;
-    const int32_t jb = next_pos < 0 ? 0 : next_pos / a.block_size;
-    next_token = next_pos - jb * a.block_size;
+    const int32_t jb = next_pos < 0 ? 0 : whole ? next_pos >> bits : next_pos / a.block_size;
+    next_token = whole ? 0 : next_pos - jb * a.block_size;
     const int32_t* from = a.q_offsets;  // (a load in every case: one under a condition would be waited for there)
     if (next_pos >= 0)
       from = next_pos < a.table_shared ? a.shared_blocks + jb : a.block_tables + int64_t(r) * a.max_blocks + jb;
@@ -498,13 +499,18 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           at_block[i] = __shfl_sync(0xffffffffu, entry, box + i);
-          at_group[i] = __shfl_sync(0xffffffffu, group, box + i);
+          at_group[i] = whole ? 0 : __shfl_sync(0xffffffffu, group, box + i);
         }
         if (elect_one()) {
+          const uint32_t step = uint32_t(D * 2) << bits, to = dst + box * step;
+          if (((good >> box) & 255u) == 255u) {  // all there, as in most tiles
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((good >> (box + i)) & 1u)
-              copy_box(dst + ((box + i) << bits) * (D * 2), map, slab, at_group[i], at_block[i], landed);
+            for (int i = 0; i < 8; ++i) copy_box(to + i * step, map, slab, at_group[i], at_block[i], landed);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((good >> (box + i)) & 1u) copy_box(to + i * step, map, slab, at_group[i], at_block[i], landed);
+          }
         }
       }
       if (clear) {
