@@ -107,6 +107,11 @@ constexpr int kKeysPerSplit = 128;
 // The shared prefix gets a grid of its own (attend_tiles over all requests'
 // rows) where the requests would otherwise read this many bytes of it.
 constexpr int64_t kSharedBytes = 64 << 20;
+// Its keys are split into parts of this many tiles, as few CTAs as that: they
+// run beside the requests' grid, which is short of bandwidth and not of SMs
+// (100 requests of 2000 keys behind 4096 shared: 171 us; with parts of 2 tiles,
+// which take every SM first, 187; of 16, which end last, 192).
+constexpr int kTilesPerPart = 8;
 constexpr int kMostParts = 16;
 
 // What an attention call launches; all from the host's numbers.
@@ -137,7 +142,7 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   if (has_tiles && !p.wide && a->num_requests > 1 && int64_t(a->shared_len) * a->num_requests * q->kv_heads * q->head_dim * 4 >= kSharedBytes) {
     p.shared_units = (rows + isq::kUnitRows - 1) / isq::kUnitRows;
     const int64_t ctas = p.shared_units * q->kv_heads, tiles = (int64_t(a->shared_len) + 127) / 128;
-    p.parts = int32_t(std::max<int64_t>(1, std::min<int64_t>({q->sm_count / ctas, (tiles + 1) / 2, kMostParts})));
+    p.parts = int32_t(std::max<int64_t>(1, std::min<int64_t>({q->sm_count / ctas, (tiles + kTilesPerPart - 1) / kTilesPerPart, kMostParts})));
     p.ml_bytes = round256(int64_t(p.parts) * a->num_tokens * a->q.num_heads * int64_t(sizeof(float2)));
     p.o_bytes = int64_t(p.parts) * a->num_tokens * a->q.num_heads * q->head_dim * int64_t(sizeof(float));
   }
