@@ -471,7 +471,6 @@ __device__ __forceinline__ void gather_tiles(const AttendArgs& a, const CUtensor
     next_entry = *from;
   };
   look_up(g / 2);
-  if (lane == 0) fetch_map(g & 1 ? v_map : k_map);
   int32_t u = g;
   for (; u < 2 * tiles; u += W) {
     const int32_t j0 = lo + (u >> 1) * kTileKeys;

@@ -78,23 +78,24 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
     return;
   }
   if (a.splits > 1) cluster_arrive();  // this CTA has started: its shared memory may be written
-  // what needs no metadata first, beside the loads of find_unit
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], 1);
-      bar_init(&bar_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bar_s[i], 1);
-      bar_init(&bar_p[i], 128);
-    }
+  // what needs no metadata first, a barrier a thread
+  if (tid < NS) {
+    bar_init(&bar_full[tid], 1);
+    bar_init(&bar_empty[tid], 1);
+  } else if (tid >= 32 && tid < 34) {
+    bar_init(&bar_s[tid - 32], 1);
+    bar_init(&bar_p[tid - 32], 128);
+  } else if (tid == 64) {
     bar_init(&bar_q, 128);
     bar_init(&bar_o, 1);
     bar_init(&bar_end, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_failed = 0;
     s_bad = 0;
+  } else if (tid == 96) {
+    fetch_map(&k_map);
+    fetch_map(&v_map);
   }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (warp == S::kProductWarp) tmem_alloc(&s_tmem, S::kColumns);
   int32_t r, tile;
   Request rq;
@@ -362,18 +363,24 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   constexpr int kLogD = D == 256 ? 8 : D == 128 ? 7 : D == 64 ? 6 : 5;
   const int share_log2 = kLogD - a.splits_log2, share = 1 << share_log2;
   const uint32_t o_at = smem_addr(join_o), ml_at = smem_addr(s_join_ml);
-  auto join_at = [&](int row, int d) {  // of (row, dim d) in the CTA that gets it
-    return in_cta(o_at + ((((split * NR + row) << share_log2) + (d & (share - 1))) << 2), d >> share_log2);
+  // of (row 0, dim d) in the CTA that gets it; rows are 4 * share bytes apart
+  auto join_at = [&](int d) {
+    return in_cta(o_at + (((split * NR << share_log2) + (d & (share - 1))) << 2), d >> share_log2);
   };
   auto join_ml = [&](int row, float m, float l, int to) {
     st_cluster2(in_cta(ml_at + (split * NR + row) * 8, to), m, l);
   };
   if (warp < 4) {
 #pragma unroll
-    for (int g = 0; g < S::kGroups; ++g)
+    for (int g = 0; g < S::kGroups; ++g) {
+      if (g * 128 + tid >= D) break;
+      const uint32_t to = join_at(g * 128 + tid);
 #pragma unroll
-      for (int c = 0; c < NR; ++c)
-        if (c < rows && g * 128 + tid < D && !s_odd[c]) st_cluster(join_at(c, g * 128 + tid), __uint_as_float(o[g][c]));
+      for (int c = 0; c < NR; ++c) {
+        if (c >= rows) break;
+        if (!s_odd[c]) st_cluster(to + (c << (share_log2 + 2)), __uint_as_float(o[g][c]));
+      }
+    }
   } else {
     for (int i = tid - 128; i < rows << a.splits_log2; i += NT - 128) {
       const int row = i >> a.splits_log2;
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
     float m, l, x[D / 32];
     row_by_keys<D>(a, r, h, q_tile, row, max(lo, a.first_key), s_lim[row], m, l, x);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) st_cluster(join_at(row, lane + 32 * i), x[i]);
+    for (int i = 0; i < D / 32; ++i) st_cluster(join_at(lane + 32 * i) + (row << (share_log2 + 2)), x[i]);
     if (lane < a.splits) join_ml(row, m, l, lane);
   }
   if (a.splits > 1) {

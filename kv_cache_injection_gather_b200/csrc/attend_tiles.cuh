@@ -153,24 +153,25 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     check_requests<S::kThreads>(a);
     return;
   }
-  // what needs no metadata first, beside the loads of find_unit
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      bar_init(&bar_full[i], 1);
-      bar_init(&bar_empty[i], 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bar_s[i], 1);
-      bar_init(&bar_p[i][0], kStreamRows);
-      bar_init(&bar_p[i][1], kStreamRows);
-      bar_init(&bar_o[i], 1);
-    }
+  // what needs no metadata first, a barrier a thread
+  if (tid < NS) {
+    bar_init(&bar_full[tid], 1);
+    bar_init(&bar_empty[tid], 2);
+  } else if (tid >= 32 && tid < 34) {
+    bar_init(&bar_s[tid - 32], 1);
+    bar_init(&bar_p[tid - 32][0], kStreamRows);
+    bar_init(&bar_p[tid - 32][1], kStreamRows);
+    bar_init(&bar_o[tid - 32], 1);
+  } else if (tid == 64) {
     bar_init(&bar_q, 2 * kStreamRows);
     bar_init(&bar_edge, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_failed = 0;
     s_bad = 0;
+  } else if (tid == 96) {
+    fetch_map(&k_map);
+    fetch_map(&v_map);
   }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (warp == S::kProductWarp) tmem_alloc(&s_tmem, 512);
   int32_t r, tile;
   Request rq;
