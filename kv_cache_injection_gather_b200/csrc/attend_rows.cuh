@@ -33,10 +33,9 @@ constexpr int kMostSplits = 8;   // CTAs of a cluster
 template <int D, int NR>
 struct RowsShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;         // one K or V tile
-  // As many slots as fit, and gather warps that divide them; with 64 rows as
-  // few warps as leave the softmax its registers.
-  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? (NR == 16 ? 6 : NR == 32 ? 5 : 4) : D == 64 ? 10 : 16;
-  static constexpr int kGather = NR == 64 ? 2 : kSlots == 16 ? 4 : kSlots == 10 ? 5 : kSlots;
+  // as many slots as fit, and gather warps that divide them
+  static constexpr int kSlots = D == 256 ? 3 : D == 128 ? 6 : D == 64 ? 10 : 16;
+  static constexpr int kGather = D == 32 ? 4 : D == 64 ? 5 : kSlots;
   static constexpr int kProductWarp = 4 + kGather;
   static constexpr int kThreads = (4 + kGather + 1) * 32;
   static constexpr int kQBytes = NR * D * 2;
@@ -46,7 +45,7 @@ struct RowsShape {
   static constexpr int kSmemBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024 + 2 * kPBytes + kJoinBytes + 1024;
   static constexpr int kGroups = (D + 127) / 128;              // O^T accumulators
   // S^T twice and O^T, as a power of two of columns
-  static constexpr int kColumns = NR == 16 ? 64 : NR == 32 ? 128 : 256;
+  static constexpr int kColumns = NR == 16 ? 64 : 128;
   static_assert((2 + kGroups) * NR <= kColumns, "tensor memory");
 };
 

@@ -18,9 +18,10 @@
 // Warps 0-3 and 4-7 do the streams' softmax, one row a thread; warps 8 on
 // gather keys and values from the cache's blocks into a ring of 128-key tiles
 // (TMA boxes of a block's tokens, in the 128-byte swizzle that the products
-// read); one thread of the last issues the products.  mbarriers join them.  Every wait is
-// bounded: a thread that gives up sets a flag that all see, the CTA drains,
-// frees its tensor memory and records IS_ERR_TIMEOUT.
+// read); the last two issue a stream's products each, from one thread.
+// mbarriers join them.  Every wait is bounded: a thread that gives up sets a
+// flag that all see, the CTA drains, frees its tensor memory and records
+// IS_ERR_TIMEOUT.
 #pragma once
 
 #include "attend_common.cuh"
@@ -47,10 +48,9 @@ struct TilesShape {
 
 // ---------------------------------------------------------------- the kernel
 
-#ifndef V_POLY
-#define V_POLY 1
-#endif
-constexpr int kPolynomial = V_POLY;  // of 8 exponentials
+// Of 8 exponentials, those on the multiply-add units.  0: 333 us for two
+// prompts of 4096 tokens (mean of two), 1: 306, 2: 314, 4: 400.
+constexpr int kPolynomial = 1;
 
 struct Yes {
   static constexpr bool value = true;
@@ -535,6 +535,48 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+}
+
+// The output of rows whose sums are in parts: one warp a row.  Rows that no
+// request owns, or a refused one, are left as they are.
+constexpr int kJoinRows = 8;  // of a CTA
+
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * 32) join_parts_kernel(const __grid_constant__ AttendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t part_rows = int64_t(a.num_tokens) * a.num_heads;
+  const int64_t row = int64_t(blockIdx.x) * kJoinRows + threadIdx.x / 32;
+  const int32_t t = int32_t(min(row, part_rows - 1) / a.num_heads), head = int32_t(row - int64_t(t) * a.num_heads);
+  Request q;
+  const bool owned =
+      row < part_rows && read_request(a, owner_of(a, t), q) == 0 && t >= q.tok0 && t < q.tok0 + q.n;
+  wait_for_previous();
+  if (!owned) return;
+  float m = neg_inf();
+  for (int k = 0; k < a.num_parts; ++k) m = fmaxf(m, __ldcg(&a.part_ml[k * part_rows + row].x));
+  const float ref = m == neg_inf() ? 0.f : m;
+  float l = 0.f, x[D / 32] = {};
+  for (int k = 0; k < a.num_parts; ++k) {
+    const float2 ml = __ldcg(&a.part_ml[k * part_rows + row]);
+    if (ml.y == 0.f) continue;  // nothing seen: the part's values mean nothing
+    const float w = exp2f(ml.x - ref);
+    l += w * ml.y;
+    const float* o = a.part_o + (k * part_rows + row) * D;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(o + 64 * i + 2 * lane));
+      x[2 * i] = fmaf(w, v.x, x[2 * i]);
+      x[2 * i + 1] = fmaf(w, v.y, x[2 * i + 1]);
+    }
+  }
+  // a sum of 0: no key was seen, or none with a score above -inf
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  uint16_t* out = a.out.data + t * a.out.ts + head * a.out.hs;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    *reinterpret_cast<uint32_t*>(out + 64 * i + 2 * lane) = none ? 0u : to_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[row] = none ? neg_inf() : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace isq

@@ -68,26 +68,27 @@ struct AttendKernel {
   void (*fn)(isq::AttendArgs, CUtensorMap, CUtensorMap);
   int smem, threads, rows;  // rows of a unit
 };
-// The streaming kernel for units of 16, 32 or 64 rows (head_dim 256: 16).
+// The streaming kernel: units of 16 rows; of 32 for head_dim 32, whose long
+// requests it takes too.
 template <int D, int NR>
 AttendKernel attend_rows_of() {
   return {&isq::attend_rows_kernel<D, NR>, isq::RowsShape<D, NR>::kSmemBytes, isq::RowsShape<D, NR>::kThreads, NR};
 }
 template <int D>
 AttendKernel attend_rows_of(int64_t most) {
-  return most <= 16 ? attend_rows_of<D, 16>() : most <= 32 ? attend_rows_of<D, 32>() : attend_rows_of<D, 64>();
+  return most <= 16 ? attend_rows_of<D, 16>() : attend_rows_of<D, 32>();
 }
 // For requests of up to `most` rows per KV head.
 AttendKernel attend_rows_of(int D, int64_t most) {
   switch (D) {
     case 32: return attend_rows_of<32>(most);
-    case 64: return attend_rows_of<64>(most);
-    case 128: return attend_rows_of<128>(most);
+    case 64: return attend_rows_of<64, 16>();
+    case 128: return attend_rows_of<128, 16>();
     default: return attend_rows_of<256, 16>();
   }
 }
 
-// The tensor-memory kernel: head_dim 64 and 128 (fn is nullptr otherwise).
+// The kernel for many rows: head_dim 64 and 128 (fn is nullptr otherwise).
 template <int D>
 AttendKernel attend_tiles_of(bool shared) {
   return {shared ? &isq::attend_tiles_kernel<D, true> : &isq::attend_tiles_kernel<D, false>,
@@ -98,12 +99,17 @@ AttendKernel attend_tiles_of(int D, bool shared) {
   if (D == 128) return attend_tiles_of<128>(shared);
   return {nullptr, 0, 0, 0};
 }
+// What joins its parts.
+using JoinKernel = void (*)(isq::AttendArgs);
+JoinKernel join_parts_of(int D) { return D == 64 ? &isq::join_parts_kernel<64> : &isq::join_parts_kernel<128>; }
 
-// Rows of a KV head and request up to which attend_rows takes them, if
-// attend_tiles could.
-constexpr int kMostNarrowRows = 64;
-// Keys that a split of a unit's keys should at least have.
+// Rows of a KV head and request up to which attend_rows takes them where
+// attend_tiles could (64 requests of 2250 keys: 32 rows take 164 us against 139,
+// 64 rows 272 against 141; attend_tiles costs as much for any number).
+constexpr int kMostNarrowRows = 16;
+// Keys that a split of a unit's keys should at least have, and a part.
 constexpr int kKeysPerSplit = 128;
+constexpr int kKeysPerPart = 512;
 // The shared prefix gets a grid of its own (attend_tiles over all requests'
 // rows) where the requests would otherwise read this many bytes of it.
 constexpr int64_t kSharedBytes = 64 << 20;
@@ -117,10 +123,11 @@ constexpr int kMostParts = 16;
 // What an attention call launches; all from the host's numbers.
 struct AttendPlan {
   bool wide;             // attend_tiles over requests, else attend_rows
-  AttendKernel kernel;
+  bool shared;           // before it, attend_tiles over the shared prefix
+  AttendKernel kernel;   // of the requests
   int64_t units;         // of the requests' grid
-  int32_t splits;        // its splits (attend_rows: a cluster)
-  int32_t parts;         // splits of the shared prefix's grid; 0: no such grid
+  int32_t splits;        // of attend_rows (a cluster)
+  int32_t parts;         // that attend_tiles writes: of the prefix, or of the requests; 0: none
   int64_t shared_units;
   int64_t ml_bytes, o_bytes;  // work space
 };
@@ -132,6 +139,7 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   const int64_t group = a->q.num_heads / q->kv_heads;
   const int64_t rows = int64_t(a->num_tokens) * group;
   const int64_t most = int64_t(std::min(a->max_q_len, a->num_tokens)) * group;
+  const int64_t keys = std::max<int64_t>(int64_t(a->max_blocks_per_req) * c->block_size, a->shared_len);
   const bool has_tiles = attend_tiles_of(q->head_dim, false).fn != nullptr;
   p.wide = has_tiles && most > kMostNarrowRows;
   p.kernel = p.wide ? attend_tiles_of(q->head_dim, false) : attend_rows_of(q->head_dim, most);
@@ -139,22 +147,36 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   // one unit per request where it holds all the request's rows, else at most
   // a partial unit per request more than the rows fill
   p.units = most <= unit_rows ? a->num_requests : (rows + unit_rows - 1) / unit_rows + a->num_requests;
-  if (has_tiles && !p.wide && a->num_requests > 1 && int64_t(a->shared_len) * a->num_requests * q->kv_heads * q->head_dim * 4 >= kSharedBytes) {
-    p.shared_units = (rows + isq::kUnitRows - 1) / isq::kUnitRows;
-    const int64_t ctas = p.shared_units * q->kv_heads, tiles = (int64_t(a->shared_len) + 127) / 128;
-    p.parts = int32_t(std::max<int64_t>(1, std::min<int64_t>({q->sm_count / ctas, (tiles + kTilesPerPart - 1) / kTilesPerPart, kMostParts})));
-    p.ml_bytes = round256(int64_t(p.parts) * a->num_tokens * a->q.num_heads * int64_t(sizeof(float2)));
-    p.o_bytes = int64_t(p.parts) * a->num_tokens * a->q.num_heads * q->head_dim * int64_t(sizeof(float));
-  }
-  // The keys of a unit are split over a cluster while the grid leaves SMs
-  // idle and a split keeps some tiles per warp.
+  const int64_t ctas = p.units * q->kv_heads;
   p.splits = 1;
-  const int64_t keys = std::max<int64_t>(int64_t(a->max_blocks_per_req) * c->block_size, a->shared_len) -
-                       (p.parts ? a->shared_len : 0);
-  if (!p.wide)
-    while (p.splits < isq::kMostSplits && p.units * q->kv_heads * p.splits < 2 * q->sm_count &&
-           keys >= int64_t(2 * p.splits) * kKeysPerSplit)
+  if (p.wide) {
+    // few CTAs: the keys of each in parts, that a grid behind joins
+    const int64_t most_parts = std::min<int64_t>({q->sm_count / ctas, keys / kKeysPerPart, kMostParts});
+    if (most_parts > 1) p.parts = int32_t(most_parts);
+  } else {
+    const int64_t prefix = int64_t(a->shared_len) * a->num_requests * q->kv_heads * q->head_dim * 4;
+    p.shared = has_tiles && a->num_requests > 1 && prefix >= kSharedBytes;
+    if (p.shared) {
+      p.shared_units = (rows + isq::kUnitRows - 1) / isq::kUnitRows;
+      const int64_t most_parts = q->sm_count / (p.shared_units * q->kv_heads);
+      const int64_t tiles = (int64_t(a->shared_len) + isq::kTileKeys - 1) / isq::kTileKeys;
+      p.parts = int32_t(std::max<int64_t>(
+          1, std::min<int64_t>({most_parts, (tiles + kTilesPerPart - 1) / kTilesPerPart, kMostParts})));
+    }
+    // The keys of a unit are split over a cluster while all splits fit the SMs
+    // at once (a CTA has one to itself and costs some 10 000 cycles of start
+    // and end: 10 requests of 2250 keys take 31 us so, and 41 with twice the
+    // CTAs).
+    const int64_t own = keys - (p.shared ? a->shared_len : 0);
+    while (p.splits < isq::kMostSplits && ctas * p.splits * 2 <= q->sm_count &&
+           own >= int64_t(2 * p.splits) * kKeysPerSplit)
       p.splits *= 2;
+  }
+  if (p.parts) {
+    const int64_t part_rows = int64_t(p.parts) * a->num_tokens * a->q.num_heads;
+    p.ml_bytes = round256(part_rows * int64_t(sizeof(float2)));
+    p.o_bytes = part_rows * q->head_dim * int64_t(sizeof(float));
+  }
   return p;
 }
 
@@ -205,13 +227,12 @@ int box_maps(const is_query* q, isq::AttendArgs& a, CUtensorMap& k, CUtensorMap&
   return box;
 }
 
-#ifndef V_NT
-#define V_NT 64
-#endif
 int launch_rows(const is_query* q, const isq::RowArgs& a, int32_t num_tokens, cudaStream_t st) {
   const int64_t want = (int64_t(std::max({a.nq, a.nk, a.nv})) * (q->head_dim / 16) + 31) / 32 * 32;
-  // few tokens: a thread a row, for latency; many: threads with several rows
-  const int most = num_tokens < 4 * q->sm_count ? isq::kRowThreads : V_NT;
+  // Few tokens: a thread a row and role, for latency.  Many: 64 threads with
+  // several rows each, whose loads are in flight together and which share a
+  // token's angles (16384 tokens, 40 normed heads: 60 us, with 128 threads 72).
+  const int most = num_tokens < 4 * q->sm_count ? isq::kRowThreads : 64;
   const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
   const unsigned threads = unsigned(std::min<int64_t>(want, most));
   rows_kernel_of(q->head_dim, q->style, norm)<<<unsigned(num_tokens), threads, 0, st>>>(a);
@@ -280,9 +301,9 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
   for (bool norm : {false, true})
     ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(
                                                 rows_kernel_of(c.head_dim, c.rope_style, norm))) == cudaSuccess;
+  ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(join_parts_of(c.head_dim))) == cudaSuccess;
   for (const AttendKernel& k : {attend_rows_of(c.head_dim, 16), attend_rows_of(c.head_dim, 32),
-                                attend_rows_of(c.head_dim, 64), attend_tiles_of(c.head_dim, false),
-                                attend_tiles_of(c.head_dim, true)})
+                                attend_tiles_of(c.head_dim, false), attend_tiles_of(c.head_dim, true)})
     ok = ok && (!k.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) == cudaSuccess);
   void* encode = nullptr;
@@ -414,7 +435,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   }
   // attend_tiles: one dimension; attend_rows: (head, split), units, more units
   const int64_t shared_grid = p.shared_units * query->kv_heads * p.parts;
-  const int64_t grid_x = p.wide ? p.units * query->kv_heads + 1 : int64_t(query->kv_heads) * p.splits;
+  const int64_t grid_x = p.wide ? p.units * query->kv_heads * std::max(1, p.parts) + 1 : int64_t(query->kv_heads) * p.splits;
   const int64_t grid_y = p.wide ? 1 : std::min<int64_t>(p.units + 1, 32768);
   const int64_t grid_z = p.wide ? 1 : (p.units + grid_y) / grid_y;
   if (grid_x > INT32_MAX || shared_grid > INT32_MAX || grid_z > 65535) return IS_ERR_CAPACITY;
@@ -450,43 +471,53 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
 
   CUtensorMap k_map{}, v_map{};
   a.box_log2 = box_maps(query, a, k_map, v_map);
+  if (p.parts) {
+    a.part_ml = static_cast<float2*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  if (p.parts) {
-    isq::AttendArgs sa = a;
-    sa.splits = p.parts;
-    sa.units = p.shared_units;
-    sa.part_ml = a.part_ml = static_cast<float2*>(workspace);
-    sa.part_o = a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ml_bytes);
-    const AttendKernel k = attend_tiles_of(query->head_dim, true);
-    cfg.gridDim = dim3(unsigned(shared_grid));
+  auto launch = [&](const AttendKernel& k, dim3 grid) {
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(k.threads));
     cfg.dynamicSmemBytes = size_t(k.smem);
-    if (cudaLaunchKernelEx(&cfg, k.fn, sa, k_map, v_map) != cudaSuccess) {
-      cudaGetLastError();
-      return IS_ERR_CUDA;
-    }
-    // the requests' grid starts beside it and waits for the parts at its end
+    return cudaLaunchKernelEx(&cfg, k.fn, a, k_map, v_map) == cudaSuccess;
+  };
+  // a grid that starts beside the one before it and waits for it at its end
+  auto beside = [&] {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  };
+  bool ok = true;
+  if (p.shared) {
+    a.splits = p.parts;
+    a.units = p.shared_units;
+    ok = launch(attend_tiles_of(query->head_dim, true), dim3(unsigned(shared_grid)));
+    beside();
     a.num_parts = p.parts;
     a.first_key = a.shared_len;
     a.table_shared = 0;  // what is left of a request is in its own blocks
   }
   a.units = p.units;
-  a.splits = p.splits;
-  while ((1 << a.splits_log2) < p.splits) ++a.splits_log2;
+  a.splits = p.wide ? std::max(1, p.parts) : p.splits;
   if (!p.wide && p.splits > 1) {
+    while ((1 << a.splits_log2) < p.splits) ++a.splits_log2;
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.splits), 1, 1};
   }
-  const AttendKernel& k = p.kernel;
-  cfg.gridDim = dim3(unsigned(grid_x), unsigned(grid_y), unsigned(grid_z));
-  cfg.blockDim = dim3(unsigned(k.threads));
-  cfg.dynamicSmemBytes = size_t(k.smem);
-  if (cudaLaunchKernelEx(&cfg, k.fn, a, k_map, v_map) != cudaSuccess) {
+  ok = ok && launch(p.kernel, dim3(unsigned(grid_x), unsigned(grid_y), unsigned(grid_z)));
+  if (p.wide && p.parts) {
+    a.num_parts = p.parts;
+    beside();
+    const int64_t rows = int64_t(a.num_tokens) * a.num_heads;
+    cfg.gridDim = dim3(unsigned((rows + isq::kJoinRows - 1) / isq::kJoinRows));
+    cfg.blockDim = dim3(isq::kJoinRows * 32);
+    cfg.dynamicSmemBytes = 0;
+    ok = ok && cudaLaunchKernelEx(&cfg, join_parts_of(query->head_dim), a) == cudaSuccess;
+  }
+  if (!ok) {
     cudaGetLastError();
     return IS_ERR_CUDA;
   }

@@ -68,6 +68,8 @@ def attend_reference(q, q_off, start, kv, tables, k_cache, v_cache, block, share
         result by about 2^-22 (|s| + 2): each p is off by a factor
         exp(2 c), c = 2^-24 (D + 2) max S + 2^-22 (max |s| + 2), in numerator
         and denominator: 4 c A;
+      * where a share of the exponentials is a polynomial within 2^-18 of them:
+        2^-17 A, in numerator and denominator;
       * sums over n keys in fp32, in any order: 2 n 2^-24 A.
     """
     T, Hq, D = q.shape
@@ -100,7 +102,7 @@ def attend_reference(q, q_off, start, kv, tables, k_cache, v_cache, block, share
             o = torch.einsum("hgn,nhd->hgd", p, V[:lim])
             A = torch.einsum("hgn,nhd->hgd", p, V[:lim].abs())
             out[t] = o.reshape(Hq, D)
-            tol[t] = (2.0 ** -8 * (o.abs() + A) + A * (4 * c[..., None] + 2 * lim * 2.0 ** -24)).reshape(Hq, D)
+            tol[t] = (2.0 ** -8 * (o.abs() + A) + A * (4 * c[..., None] + 2.0 ** -17 + 2 * lim * 2.0 ** -24)).reshape(Hq, D)
             lse[t] = torch.logsumexp(s, -1).reshape(Hq)
         del jj
     return out, lse, tol

@@ -276,6 +276,173 @@ def test_attend_long_shared_prefix(pkg, requests, n):
     check_attend(pkg, Paged(8, 128, 2, 4, 16, [n] * requests, mem, shared=2050, qscale=2.0))
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("n,G", [(5, 4), (8, 4), (9, 7), (16, 4), (1, 40), (17, 4)])
+def test_attend_a_few_tokens(pkg, D, n, G):
+    """Units of 17 to 64 rows (and just past), with prefixes and splits."""
+    check_attend(pkg, Paged(20 + n, D, 1, G, 16, [n, max(1, n - 3)], [5, 700], 90))
+    check_attend(pkg, Paged(21 + n, D, 2, G, 32, [n], [1900], 0, head_major=True))
+
+
+@pytest.mark.parametrize("D,block", [(256, 128), (32, 64), (64, 8), (128, 40)])
+def test_attend_block_sizes(pkg, D, block):
+    check_attend(pkg, Paged(30 + D, D, 3, 2, block, [1, 20, 3], [1, 300, 129], 0))
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 7), (128, 1)])
+@pytest.mark.parametrize("shared,block", [(2048, 16), (1999, 16), (1030, 24), (1501, 1)])
+def test_attend_prefix_in_a_grid_of_its_own(pkg, D, G, shared, block):
+    """A prefix long enough, over enough requests, to be attended to once for
+    all of them: requests that see less than the prefix, exactly it, one key
+    more, nothing; one to a few queries; rows behind the last request."""
+    R, H = 48, 4
+    n = [1 + (r % 3 if G < 7 else 0) for r in range(R)]
+    kv = [shared + n[r] + (37 * r) % 150 for r in range(R)]
+    kv[3], kv[5], kv[7], kv[9], kv[11] = 0, 1, shared, shared + 1, shared // 2
+    start = [max(0, k - m) for k, m in zip(kv, n)]
+    start[9] = shared + 40
+    # what decides, with the call's numbers
+    assert shared * R * H * D * 4 >= 64 << 20 or D == 64
+    for causal in (True, False):
+        c = Paged(shared + G, D, H, G, block, n, [0] * R, shared=shared, kv=kv, start=start, extra_rows=3, qscale=1.5)
+        check_attend(pkg, c, causal)
+
+
+def test_prefix_grid_masked_values_and_bad_blocks(pkg):
+    R, H, G, D, shared = 40, 4, 4, 128, 2000
+    kv = [shared + 50 + r for r in range(R)]
+    kv[2] = 700  # its queries see positions up to 699 of the prefix
+    c = Paged(77, D, H, G, 16, [1] * R, [0] * R, shared=shared, kv=kv)
+    with make(pkg, D, H) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        clean = c.call(s, cache)
+        again = c.call(s, cache)
+        assert torch.equal(clean, again)  # the same bits every time
+        ref, _, tol = c.reference()
+        within(clean, ref, tol)
+        b, o = int(c.shared_blocks[750 // 16]), 750 % 16  # in a tile of request 2's, past its limit
+        c.v[b, o, 1, 9] = math.nan
+        c.k[b, o, 2, 3] = math.inf
+        c.sync_cache()
+        got = c.call(s, cache)
+        within(got[2:3], ref[2:3], tol[2:3])
+        assert not torch.isfinite(got[3, G:2 * G, 9]).any()
+        c.v[b, o, 1, 9] = 0.5
+        c.k[b, o, 2, 3] = 0.25
+        c.sync_cache()
+        good = c.call(s, cache)
+        # a block of the prefix outside the cache: left out for all
+        old = c.shared_blocks
+        c.shared_blocks = old.clone()
+        c.shared_blocks[10] = -3
+        out = c.call(s, cache)
+        assert s.last_query_error() == (pkg.IS_ERR_BAD_BLOCK, -1)
+        keep = torch.tensor([j for j in range(kv[0]) if not 160 <= j < 176])
+        table = torch.where(keep < shared, old[(keep // 16).clamp(max=len(old) - 1)], c.tables[0, keep // 16])
+        K, V = c.k[table.long(), keep % 16].double(), c.v[table.long(), keep % 16].double()
+        p = torch.softmax(torch.einsum("hgd,nhd->hgn", c.q[0].double().view(H, G, D), K) / math.sqrt(D), -1)
+        want = torch.einsum("hgn,nhd->hgd", p, V).reshape(H * G, D)
+        # summed key by key in fp32: the result's rounding alone is larger
+        assert ((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -12).all()
+        # one of a request's own blocks: that request alone
+        c.shared_blocks = old
+        t = c.tables
+        c.tables = t.clone()
+        c.tables[5, 2010 // 16] = 10 ** 9
+        out = c.call(s, cache)
+        assert s.last_query_error() == (pkg.IS_ERR_BAD_BLOCK, 5)
+        rest = [r for r in range(R) if r != 5]
+        assert torch.equal(out[rest], good[rest]) and torch.isfinite(out[5]).all()
+
+
+def test_prefix_grid_in_place_in_a_graph_and_on_two_streams(pkg):
+    R, H, G, D, shared = 64, 2, 4, 128, 3000
+    c = Paged(78, D, H, G, 16, [1] * R, [(11 * r) % 300 for r in range(R)], shared=shared)
+    assert shared * R * H * D * 4 >= 64 << 20
+    with make(pkg, D, H) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        ref, _, tol = c.reference()
+        want = c.call(s, cache)
+        within(want, ref, tol)
+        q = c.q.clone()
+        keep, c.q = c.q, q
+        assert torch.equal(c.call(s, cache, out=q), want)
+        c.q = keep
+        meta = (c.i32(c.q_off), c.i32(c.start), c.i32(c.kv), c.tables.cuda(), cache, c.layer)
+        kw = dict(max_q_len=1, shared_blocks=c.shared_blocks.cuda(), shared_len=shared)
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        graphs, outs = [], []
+        for st in streams:
+            o = torch.zeros_like(want)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                s.attend(c.q, *meta, out=o, **kw)
+            graphs.append(g), outs.append(o)
+        for _ in range(5):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        eager = [s.attend(c.q, *meta, stream=st.cuda_stream, **kw) for st in streams for _ in range(3)]
+        torch.cuda.synchronize()
+        assert s.last_query_error() == (0, 0)
+        for o in outs + eager:
+            assert torch.equal(o, want)
+        del graphs
+
+
+@pytest.mark.parametrize("n", [1, 24, 80])
+def test_offsets_past_32_bits(pkg, n):
+    """Blocks 2^27 elements apart: element offsets past 2^32."""
+    H, G, D, B, nb = 1, 4, 128, 16, 40
+    stride = 1 << 27
+    big = [torch.empty(stride * (nb - 1) + B * H * D, dtype=BF, device="cuda") for _ in range(2)]
+    kc, vc = (x.as_strided((1, nb, B, H, D), (0, stride, H * D, D, 1)) for x in big)
+    c = Paged(79, D, H, G, B, [n], [nb * B - n - 60], layers=1, layer=0, spare=0 if n > 1 else 3)
+    blocks = c.k.shape[0]
+    assert blocks <= nb
+    kc[0, :blocks], vc[0, :blocks] = c.k, c.v
+    c.k_cache, c.v_cache = kc, vc
+    assert int(c.tables.max()) * stride > 2 ** 32
+    check_attend(pkg, c)
+    with make(pkg, D, H, layers=1) as s:
+        k, v = (torch.randn(2, H, D, device="cuda").to(BF) for _ in range(2))
+        slots = torch.tensor([(nb - 1) * B + 3, 36 * B], device="cuda")
+        s.append(k, v, c.i32([0, 0]), slots, pkg.cache_desc(kc, vc))
+        assert s.last_query_error() == (0, 0)
+        assert torch.equal(vc[0, nb - 1, 3], v[0]) and torch.equal(kc[0, 36, 0], k[1])
+
+
+def test_attend_uneven_splits(pkg):
+    """A cluster's splits where some have no keys, next to a long request."""
+    check_attend(pkg, Paged(80, 128, 2, 4, 16, [1, 1, 1], [0, 3000, 200]))
+    check_attend(pkg, Paged(81, 256, 1, 4, 16, [1, 2], [1, 1500], kv=[0, 1501]))
+
+
+def test_workspace_is_checked(pkg):
+    from kv_cache_injection_gather_b200 import binding as B
+    R, H, G, D, shared = 64, 2, 4, 128, 3000
+    c = Paged(82, D, H, G, 16, [1] * R, [5] * R, shared=shared)
+    with make(pkg, D, H) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        out = torch.zeros(R, H * G, D, dtype=BF, device="cuda")
+        sb, tables = c.shared_blocks.cuda(), c.tables.cuda()
+        ints = [c.i32(x) for x in (c.q_off, c.start, c.kv)]
+        rows = lambda t: B.is_rows_t(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])  # noqa: E731
+        args = B.is_attend_t(R, R, 1, tables.shape[1], *[t.data_ptr() for t in ints], tables.data_ptr(), sb.data_ptr(),
+                             shared, 1, 0.0, c.layer, rows(c.q), rows(out), None)
+        need = B.is_query_attend_workspace(s.query, args, cache)
+        assert need >= R * H * G * (D * 4 + 8)
+        work = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+        for ptr, size, rc in ((None, need, pkg.IS_ERR_INVALID_ARG), (work.data_ptr() + 16, need, pkg.IS_ERR_INVALID_ARG),
+                              (work.data_ptr(), need - 1, pkg.IS_ERR_CAPACITY)):
+            with pytest.raises(pkg.InjectError) as e:
+                B.is_query_attend(s.query, args, cache, ptr, size, torch.cuda.current_stream().cuda_stream)
+            assert e.value.status == rc
+        B.is_query_attend(s.query, args, cache, work.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(out, c.call(s, cache))
+
+
 def test_attend_many_requests(pkg):
     """More requests than one pass of the tile search covers, some empty."""
     n = [(7 * r) % 9 if r % 5 else 0 for r in range(700)]
