@@ -155,6 +155,8 @@ int is_query_attend_workspace(const is_query_t* query, const is_attend_t* args,
  *                shared_len (request skipped, detail: request)
  *   BAD_BLOCK    a block that is read lies outside [0, num_blocks): its
  *                keys are left out (detail: request, or -1 for a shared one)
+ *   TIMEOUT      a wait inside a kernel gave up (seconds; a fault of the
+ *                library, the call's rows are undefined)
  * A skipped request's rows are left as they were.  Requests whose token
  * ranges overlap (a decreasing offset elsewhere) have undefined rows.
  * Errors: INVALID_ARG, CAPACITY (workspace too small, or more than 2^31 - 1

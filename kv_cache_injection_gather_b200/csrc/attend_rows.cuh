@@ -16,12 +16,18 @@
 //
 // so that a tile costs the softmax threads, one key each, NR values and not a
 // padded 128 (mma.sync over 16-row tiles spent 2900 cycles a warp and 32-key
-// tile on B200, an SM's whole share of the bandwidth).  Warps 0-3 do the
-// softmax; warp 4 gathers keys and values, as TMA boxes of a block's tokens,
-// into a ring that keeps 128-192 KB in flight; one thread of warp 5 issues
-// the products, the next tile's scores ahead of this tile's sums.  The keys of
-// a unit can be split over a cluster, whose CTAs join their sums through
-// distributed shared memory.
+// tile, an SM's whole share of the bandwidth).  Warps 0-3 do the softmax; the
+// next bring keys and values, as TMA boxes of a block's tokens, into a ring
+// of up to 192 KB; one thread of the last warp issues the products, the next
+// tile's scores ahead of this tile's sums.  The keys of a unit can be split
+// over a cluster, whose CTAs join their sums through distributed shared memory.
+//
+// Measured on B200 (32 query and 8 KV heads of 128, block 16): 100 requests of
+// 800-3200 keys 141 us, 5.8 TB/s of keys and values, 0.90 of the copy
+// bandwidth; 3 requests of 60-131 k keys (4 KV heads, clusters of 8: 96 of 148
+// SMs) 126 us, 5.0 TB/s.  A tile costs an SM some 1500 cycles, of 2200 that its
+// share of the bandwidth leaves; a unit's start and end cost some 10 000, which
+// is what bounds requests of a few hundred keys (100 of 550: 70 us, 3.3 TB/s).
 #pragma once
 
 #include "attend_common.cuh"
@@ -270,24 +276,21 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
         if (t > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_o, (t - 1) & 1, &s_failed));
         if (t > 0 && ok) {
           tc_fence_after();
-          constexpr int kPiece = NR < 32 ? NR : 32;  // columns at a time
+          float shrink[NR];
 #pragma unroll
-          for (int c0 = 0; c0 < NR; c0 += kPiece) {
-            float shrink[kPiece];
+          for (int c = 0; c < NR; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&s_shrink[c]);
+            shrink[c] = f.x, shrink[c + 1] = f.y, shrink[c + 2] = f.z, shrink[c + 3] = f.w;
+          }
 #pragma unroll
-            for (int c = 0; c < kPiece; c += 4) *reinterpret_cast<float4*>(&shrink[c]) =
-                *reinterpret_cast<const float4*>(&s_shrink[c0 + c]);
+          for (int c = 0; c < NR; ++c) l[c] *= shrink[c];
 #pragma unroll
-            for (int c = 0; c < kPiece; ++c) l[c0 + c] *= shrink[c];
+          for (int g = 0; g < S::kGroups; ++g) {
+            tmem_ld<NR>(tmem_o + g * NR + lanes, v);
+            tmem_wait_ld();
 #pragma unroll
-            for (int g = 0; g < S::kGroups; ++g) {
-              uint32_t o[kPiece];
-              tmem_ld<kPiece>(tmem_o + g * NR + c0 + lanes, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < kPiece; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * shrink[c]);
-              tmem_st<kPiece>(tmem_o + g * NR + c0 + lanes, o);
-            }
+            for (int c = 0; c < NR; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * shrink[c]);
+            tmem_st<NR>(tmem_o + g * NR + lanes, v);
           }
           tmem_wait_st();
         }

