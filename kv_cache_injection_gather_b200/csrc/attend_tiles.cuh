@@ -23,16 +23,21 @@
 // flag that all see, the CTA drains, frees its tensor memory and records
 // IS_ERR_TIMEOUT.
 //
+// A tile goes through a stream in halves of 64 keys: while one half's softmax
+// runs, the products of the other are under way -- its values', and behind them
+// the next tile's scores.
+//
 // Measured on B200 (32 query and 8 KV heads of 128): two causal prompts of
-// 4096 tokens 305-340 us (790-880 TFLOP/s, 0.48-0.53 of the burst bf16 GEMM;
+// 4096 tokens 280-310 us (870-960 TFLOP/s, 0.52-0.57 of the burst bf16 GEMM;
 // the spread is the card's power limit), 100 requests of 16-64 queries over
-// 3300-5000 keys 412 us (645 TFLOP/s of what is not masked or padded).  A tile
-// of both streams takes some 3500 cycles: 2300 of products (their operands'
-// shared-memory reads; at 128 x 128 x 16 both sides are read for 64 cycles of
-// work) and, in series for a stream, load 150, maximum 350, exponentials 1300
-// (the special-function units' 1024), the products 1300.  With two streams
-// that is what bounds it; a third does not fit the tensor memory.  A unit's
-// start and end cost 15 000 cycles, of 65 000 for 4096 keys.
+// 3300-5000 keys 385 us (690 TFLOP/s of what is not masked or padded); with a
+// tile as one piece 303-328 and 412 us.  The products of a tile of both streams
+// take 2300 cycles (their operands' shared-memory reads; at 128 x 128 x 16 both
+// sides are read for 64 cycles of work), its exponentials 2048 on the
+// special-function units less the share below, with the loads, the maximum and
+// the conversions beside them on the same warps: two streams do not hide all of
+// that, and a third does not fit the tensor memory.  A unit's start and end
+// cost 15 000 cycles, of some 60 000 for 4096 keys.
 #pragma once
 
 #include "attend_common.cuh"
@@ -46,9 +51,11 @@ template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 4 : 8;
-  // 12 warps, as that leaves a thread 168 registers: a softmax thread keeps a
-  // row of 128 scores.  One warp a stream issues its products: a wait costs a
-  // lone thread some 200 cycles of latency, and a tile has four.
+  // 12 warps, as that leaves a thread 168 registers to run ahead with
+  // (100 requests of 16-64 queries: with
+  // 4 gather warps 396 us, 2: 385, 1: 476).  One warp a stream issues its
+  // products: a wait costs a lone thread some 200 cycles of latency, and a tile
+  // has four.
   static constexpr int kGather = 2;
   static constexpr int kProductWarp = 8 + kGather;       // and the next
   static constexpr int kThreads = (8 + kGather + 2) * 32;
@@ -59,9 +66,10 @@ struct TilesShape {
 
 // ---------------------------------------------------------------- the kernel
 
-// Of 8 exponentials, those on the multiply-add units.  0: 333 us for two
-// prompts of 4096 tokens (mean of two), 1: 306, 2: 314, 4: 400.
-constexpr int kPolynomial = 1;
+// Of 8 exponentials, those on the multiply-add units.  100 requests of 16-64
+// queries, with 4 gather warps 0: 408 us, 1: 401, 2: 396, 3: 398; with 2 gather
+// warps 1: 389, 2: 385, 3: 385.
+constexpr int kPolynomial = 2;
 
 struct Yes {
   static constexpr bool value = true;
@@ -148,7 +156,8 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   using S = TilesShape<D>;
   constexpr int CPR = D / 8, NS = S::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2][2], bar_o[2], bar_edge;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2][2], bar_p[2][2], bar_o[2][2],
+      bar_end[2], bar_edge;
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -169,10 +178,12 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     bar_init(&bar_full[tid], 1);
     bar_init(&bar_empty[tid], 2);
   } else if (tid >= 32 && tid < 34) {
-    bar_init(&bar_s[tid - 32], 1);
-    bar_init(&bar_p[tid - 32][0], kStreamRows);
-    bar_init(&bar_p[tid - 32][1], kStreamRows);
-    bar_init(&bar_o[tid - 32], 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bar_s[tid - 32][i], 1);
+      bar_init(&bar_p[tid - 32][i], kStreamRows);
+      bar_init(&bar_o[tid - 32][i], 1);
+    }
+    bar_init(&bar_end[tid - 32], 1);
   } else if (tid == 64) {
     bar_init(&bar_q, 2 * kStreamRows);
     bar_init(&bar_edge, 1);
@@ -261,21 +272,22 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         tc_commit(&bar_empty[at]);
         if (!by_rows) tc_commit(&bar_empty[at]);
       };
-      auto scores = [&](int at) {
+      // scores of half a tile, its 64 keys from 64 * half on
+      auto scores = [&](int at, int half) {
         tc_fence_after();
-        const uint32_t ka = ring_at + at * S::kSlotBytes;
+        const uint32_t ka = ring_at + at * S::kSlotBytes + half * (S::kSlotBytes / 2);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(ts, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
-                 product(kTileKeys, false, false), k > 0);
-        tc_commit(&bar_s[st]);
-        free_slot(at);
+          mma_ss(ts + half * 64, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
+                 product(kTileKeys / 2, false, false), k > 0);
+        tc_commit(&bar_s[st][half]);
+        if (half == 1) free_slot(at);
       };
       bool ok = bar_wait(&bar_q, 0, &s_failed) && bar_wait(&bar_full[slot], parity, &s_failed);
-      // the second stream starts half a turn late, so that one's softmax runs
-      // beside the other's products
-      if (st == 1) ok = ok && bar_wait(&bar_p[0][1], 0, &s_failed);
-      if (ok) scores(slot);
+      if (ok) {
+        scores(slot, 0);
+        scores(slot, 1);
+      }
       for (int32_t i = 0; i < n && ok; ++i) {
         advance();
         const bool more = i + 1 < n;
@@ -284,24 +296,26 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
              (!more || bar_wait(&bar_full[next], next_parity, &s_failed));
         const uint32_t va = ring_at + (slot + 1) * S::kSlotBytes;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // P comes in halves of 64 keys
+        for (int half = 0; half < 2; ++half) {
           ok = ok && bar_wait(&bar_p[st][half], i & 1, &s_failed);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k)
-            mma_ts(to, ts + k * 8, operand<D>(va + k * (D * 32), kSlabStep), product(D, false, true), i > 0 || k > 0);
+          for (int k = 0; k < 4; ++k)
+            mma_ts(to, ts + half * 64 + k * 8, operand<D>(va + (4 * half + k) * (D * 32), kSlabStep),
+                   product(D, false, true), i > 0 || half > 0 || k > 0);
+          tc_commit(&bar_o[st][half]);
+          if (half == 1) free_slot(slot + 1);
+          // (the next scores overwrite the probabilities that these products
+          // read: products run in the order of their issue)
+          if (more) scores(next, half);
         }
         if (!ok) break;
-        free_slot(slot + 1);
-        // (the next scores overwrite the probabilities that these products
-        // read: products run in the order of their issue)
-        if (more) scores(next);
         slot = next;
         parity = next_parity;
       }
-      tc_commit(&bar_o[st]);
-      bar_wait(&bar_o[st], 0, nullptr);  // nothing in flight beyond this point
+      tc_commit(&bar_end[st]);
+      bar_wait(&bar_end[st], 0, nullptr);  // nothing in flight beyond this point
     }
     __syncwarp();
   } else {
@@ -326,28 +340,29 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     const int32_t lim_min = __reduce_min_sync(0xffffffffu, lim);
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes a warp
     const uint32_t ts = tmem + st * 128 + lanes, to = tmem_o + st * OC + lanes;
-    const int32_t n = tiles_of(st);
+    const int32_t n = 2 * tiles_of(st);  // halves
     for (int32_t it = 0; it < n; ++it) {
+      const int half = it & 1;
       // the whole warp goes on or stops: what follows is warp-wide
-      if (!__all_sync(0xffffffffu, bar_wait(&bar_s[st], it & 1, &s_failed))) break;
+      if (!__all_sync(0xffffffffu, bar_wait(&bar_s[st][half], (it >> 1) & 1, &s_failed))) break;
       tc_fence_after();
-      const int32_t j0 = first_key_of(st, it);
-      const bool masked = j0 + kTileKeys > lim_min;
+      const int32_t j0 = first_key_of(st, it >> 1) + half * 64;
+      const bool masked = j0 + 64 > lim_min;
       const int32_t seen = lim - j0;  // columns below are seen
-      uint32_t v[kTileKeys];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+      const uint32_t tp = ts + half * 64;
+      uint32_t v[64];
+      tmem_ld<64>(tp, v);
       tmem_wait_ld();
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < kTileKeys; ++i)
+        for (int i = 0; i < 64; ++i)
           if (i >= seen) v[i] = 0xff800000u;
       }
       float tops[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 4]));
 #pragma unroll
-      for (int i = 8; i < kTileKeys; i += 8)
+      for (int i = 8; i < 64; i += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(v[i + e]), __uint_as_float(v[i + 4 + e]));
       // (the scale is positive: the maximum's place is the same)
@@ -360,10 +375,12 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         shrink = exp2_fast(m - top);
         m = top;
       }
-      // the products with V up to this stream's previous tile are done: the
-      // barrier's arrival followed them
       if (it > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
         l *= shrink;
+        // the products with V up to the half before (those before it are done:
+        // this half's scores were issued behind them)
+        if (!__all_sync(0xffffffffu, bar_wait(&bar_o[st][half ^ 1], ((it - 1) >> 1) & 1, &s_failed))) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t o[16];
@@ -383,30 +400,27 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       // keys are masked none are (a masked key has to be 0 exactly).
       auto probabilities = [&](auto plain) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int c = 2 * half; c < 2 * half + 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = c * 32 + 2 * i;
-              const Two x = fma2(two(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), scale2, ref2);
-              Two e;
-              if (!decltype(plain)::value && i % 8 < kPolynomial) {
-                e = exp2_two(x);
-              } else {
-                const float2 f = both(x);
-                e = two(exp2_fast(f.x), exp2_fast(f.y));
-              }
-              sum2 = add2(sum2, e);
-              p[i] = to_bf16x2(e);
+          for (int i = 0; i < 16; ++i) {
+            const int at = c * 32 + 2 * i;
+            const Two x = fma2(two(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), scale2, ref2);
+            Two e;
+            if (!decltype(plain)::value && i % 8 < kPolynomial) {
+              e = exp2_two(x);
+            } else {
+              const float2 f = both(x);
+              e = two(exp2_fast(f.x), exp2_fast(f.y));
             }
-            tmem_st16(ts + c * 16, p);
+            sum2 = add2(sum2, e);
+            p[i] = to_bf16x2(e);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          bar_arrive(&bar_p[st][half]);
+          tmem_st16(tp + c * 16, p);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        bar_arrive(&bar_p[st][half]);
       };
       if (masked) probabilities(Yes());
       else probabilities(No());
