@@ -54,7 +54,8 @@ int is_query_last_error(is_query_t* query, void* stream, int64_t* detail_out);
 /* Rows of head vectors: element (token t, head h, dim d) is
  * ((uint16_t*)data)[t*token_stride + h*head_stride + d].  Strides in
  * elements, multiples of 8; data 16-byte aligned.  A slice of a fused
- * projection's output is such rows. */
+ * projection's output is such rows.  A stride of 0 repeats a row of an input;
+ * for rows that are written it is refused (INVALID_ARG). */
 typedef struct {
   void* data;
   int64_t token_stride;
@@ -152,15 +153,16 @@ int is_query_attend_workspace(const is_query_t* query, const is_attend_t* args,
  *                that has more than max_q_len queries, or a negative
  *                start_pos or kv_len (request skipped, detail: request)
  *   POSITION     kv_lens[r] past max_blocks_per_req * block_size and past
- *                shared_len (request skipped, detail: request)
+ *                shared_len, or above 2^31 - 129 (request skipped, detail:
+ *                request)
  *   BAD_BLOCK    a block that is read lies outside [0, num_blocks): its
  *                keys are left out (detail: request, or -1 for a shared one)
  *   TIMEOUT      a wait inside a kernel gave up (seconds; a fault of the
  *                library, the call's rows are undefined)
  * A skipped request's rows are left as they were.  Requests whose token
  * ranges overlap (a decreasing offset elsewhere) have undefined rows.
- * Errors: INVALID_ARG, CAPACITY (workspace too small, or more than 2^31 - 1
- * rows of num_tokens * heads), CUDA. */
+ * Errors: INVALID_ARG, CAPACITY (workspace too small, more than 2^31 - 1
+ * rows of num_tokens * heads, or shared_len above 2^31 - 129), CUDA. */
 int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t* cache,
                     void* workspace, int64_t workspace_bytes, void* stream);
 

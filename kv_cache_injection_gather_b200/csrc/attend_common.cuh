@@ -294,6 +294,9 @@ struct Request {
   int32_t start, kv;    // position of the first, keys in the cache
 };
 
+// Positions of a request: a tile more still counts in 31 bits.
+constexpr int32_t kMostKeys = INT32_MAX - 128;
+
 // Reads request r; 0, or the error that makes the batch skip it.
 __device__ __forceinline__ int32_t read_request(const AttendArgs& a, int32_t r, Request& q) {
   const int32_t t0 = a.q_offsets[r], t1 = a.q_offsets[r + 1];
@@ -303,7 +306,7 @@ __device__ __forceinline__ int32_t read_request(const AttendArgs& a, int32_t r, 
   q.n = t1 - t0;
   if (t0 < 0 || t1 < t0 || t1 > a.num_tokens || q.n > a.max_q_len || q.start < 0 || q.kv < 0)
     return kErrInvalidArg;
-  if (q.kv > a.shared_len && q.kv > int64_t(a.max_blocks) * a.block_size) return kErrPosition;
+  if (q.kv > kMostKeys || (q.kv > a.shared_len && q.kv > int64_t(a.max_blocks) * a.block_size)) return kErrPosition;
   return 0;
 }
 

@@ -51,11 +51,10 @@ template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 4 : 8;
-  // 12 warps, as that leaves a thread 168 registers to run ahead with
-  // (100 requests of 16-64 queries: with
-  // 4 gather warps 396 us, 2: 385, 1: 476).  One warp a stream issues its
-  // products: a wait costs a lone thread some 200 cycles of latency, and a tile
-  // has four.
+  // 12 warps, as that leaves a thread 168 registers to run ahead with (100
+  // requests of 16-64 queries: with 4 gather warps 396 us, 2: 385, 1: 476).  One
+  // warp a stream issues its products: a wait costs a lone thread some 200
+  // cycles of latency, and a tile has four.
   static constexpr int kGather = 2;
   static constexpr int kProductWarp = 8 + kGather;       // and the next
   static constexpr int kThreads = (8 + kGather + 2) * 32;
@@ -396,8 +395,9 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
       Two sum2 = 0;
       // P, two keys at a time, over the scores (which are all read).  A share
       // of the exponentials is computed on the multiply-add units, as the
-      // special-function unit's 16 a cycle are what a tile waits for; where
-      // keys are masked none are (a masked key has to be 0 exactly).
+      // special-function unit's 16 a cycle are what a tile waits for; none where
+      // keys are masked, or a row has no score above -inf yet (the polynomial
+      // ends at 2^-126, and these have to be 0 exactly).
       auto probabilities = [&](auto plain) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         tc_fence_before();
         bar_arrive(&bar_p[st][half]);
       };
-      if (masked) probabilities(Yes());
+      if (masked || __any_sync(0xffffffffu, m == neg_inf())) probabilities(Yes());
       else probabilities(No());
       const float2 sums = both(sum2);
       l += sums.x + sums.y;

@@ -185,6 +185,10 @@ bool rows_ok(const is_rows_t* r) {
   return r && r->data && aligned16(r->data) && r->num_heads > 0 && r->token_stride >= 0 && r->head_stride >= 0 &&
          r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
+// Rows that are written: no two at one place by a stride of 0.
+bool out_ok(const is_rows_t* r, int32_t num_tokens) {
+  return rows_ok(r) && (r->token_stride > 0 || num_tokens == 1) && (r->head_stride > 0 || r->num_heads == 1);
+}
 isq::Rows rows_of(const is_rows_t& r) {
   return {static_cast<uint16_t*>(r.data), r.token_stride, r.head_stride};
 }
@@ -249,11 +253,11 @@ int check_attend(const is_query* q, const is_attend_t* a, const is_cache_t* c) {
   if (a->q.num_heads <= 0 || a->q.num_heads % q->kv_heads != 0 || a->out.num_heads != a->q.num_heads)
     return IS_ERR_INVALID_ARG;
   if (a->num_tokens > 0 && a->num_requests > 0) {
-    if (!rows_ok(&a->q) || !rows_ok(&a->out) || !a->q_offsets || !a->start_pos || !a->kv_lens || a->max_q_len < 1 ||
+    if (!rows_ok(&a->q) || !out_ok(&a->out, a->num_tokens) || !a->q_offsets || !a->start_pos || !a->kv_lens || a->max_q_len < 1 ||
         (a->max_blocks_per_req > 0 && !a->block_tables) || (a->shared_len > 0 && !a->shared_blocks))
       return IS_ERR_INVALID_ARG;
   }
-  if (int64_t(a->num_tokens) * a->q.num_heads > INT32_MAX) return IS_ERR_CAPACITY;
+  if (int64_t(a->num_tokens) * a->q.num_heads > INT32_MAX || a->shared_len > isq::kMostKeys) return IS_ERR_CAPACITY;
   return IS_OK;
 }
 
@@ -348,10 +352,10 @@ int is_query_rotate(is_query_t* query, int32_t num_tokens, const int32_t* positi
                     const void* k_weight, float eps, void* stream) {
   if (!query || num_tokens < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return IS_ERR_INVALID_ARG;
   if (num_tokens == 0) return IS_OK;
-  if (!positions || !rows_ok(q) || !rows_ok(q_out) || q->num_heads != q_out->num_heads || !aligned16(q_weight) ||
+  if (!positions || !rows_ok(q) || !out_ok(q_out, num_tokens) || q->num_heads != q_out->num_heads || !aligned16(q_weight) ||
       !aligned16(k_weight) || (k == nullptr) != (k_out == nullptr))
     return IS_ERR_INVALID_ARG;
-  if (k && (!rows_ok(k) || !rows_ok(k_out) || k->num_heads != k_out->num_heads)) return IS_ERR_INVALID_ARG;
+  if (k && (!rows_ok(k) || !out_ok(k_out, num_tokens) || k->num_heads != k_out->num_heads)) return IS_ERR_INVALID_ARG;
   OnDevice guard(query->device);
   isq::RowArgs a{};
   a.positions = positions;
@@ -382,7 +386,7 @@ int is_query_append(is_query_t* query, int32_t num_tokens, const int32_t* positi
       v->num_heads != query->kv_heads || !aligned16(k_weight) || !aligned16(q_weight) ||
       (q == nullptr) != (q_out == nullptr))
     return IS_ERR_INVALID_ARG;
-  if (q && (!rows_ok(q) || !rows_ok(q_out) || q->num_heads != q_out->num_heads)) return IS_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q) || !out_ok(q_out, num_tokens) || q->num_heads != q_out->num_heads)) return IS_ERR_INVALID_ARG;
   OnDevice guard(query->device);
   isq::RowArgs a{};
   a.positions = positions;

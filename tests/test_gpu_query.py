@@ -606,6 +606,63 @@ def test_attend_host_refusals(pkg):
             s.append(x[:, :2], x[:, :2], c.i32([0, 1]), torch.zeros(2, dtype=torch.int64, device="cuda"), cache, 5)
 
 
+@pytest.mark.parametrize("n,R,shared", [(1, 3, 0), (70, 3, 0), (1, 64, 3000)])
+def test_attend_scores_all_minus_infinity(pkg, n, R, shared):
+    """Rows whose every score is -inf get zeros, as rows that see no key."""
+    c = Paged(91, 128, 2, 4, 16, [n] * R, [300] * R, shared=shared)
+    for x in (c.k, c.k_cache):
+        x[~torch.isnan(x)] = 0
+        x[..., 5] = -3e38
+    c.q.zero_()
+    c.q[:, ::2, 5] = 3e38  # even heads: 3e38 * -3e38; odd ones: 0, so the values' mean
+    with make(pkg, 128, 2) as s:
+        lse = torch.zeros(c.q.shape[:2], device="cuda")
+        out = c.call(s, pkg.cache_desc(c.k_cache, c.v_cache), False, lse=lse)
+        assert s.last_query_error() == (0, 0)
+    assert (out[:, ::2] == 0).all() and (lse[:, ::2] == -math.inf).all()
+    c.q.zero_()
+    ref, rl, tol = c.reference(False)
+    within(out[:, 1::2], ref[:, 1::2], tol[:, 1::2])
+    assert torch.allclose(lse[:, 1::2].double(), rl[:, 1::2], atol=2.0 ** -14)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_attend_refuses_lengths_that_tiles_cannot_count(pkg, n):
+    c = Paged(92, 64, 2, 4, 128, [n, n], [40, 50])
+    with make(pkg, 64, 2) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        clean = c.call(s, cache)
+        blocks = 2 ** 31 // 128
+        tables = torch.zeros(2, blocks, dtype=torch.int32)
+        tables[:, :c.width] = c.tables
+        c.tables, c.kv = tables, [2 ** 31 - 128, c.kv[1]]
+        out = torch.full_like(clean, 4.0)
+        c.call(s, cache, out=out)
+        assert s.last_query_error() == (pkg.IS_ERR_POSITION, 0)
+        assert (out[:n] == 4).all() and torch.equal(out[n:], clean[n:])
+        with pytest.raises(pkg.InjectError) as e:
+            c.call(s, cache, shared_len=2 ** 31 - 128, shared_blocks=tables[0].cuda())
+        assert e.value.status == pkg.IS_ERR_CAPACITY
+
+
+def test_written_rows_of_stride_zero_are_refused(pkg):
+    c = Paged(93, 64, 2, 2, 16, [1, 1], [9, 30])
+    with make(pkg, 64, 2) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        pos, slots = c.i32([0, 1]), torch.tensor([-1, -1], device="cuda")
+        one = torch.zeros(2, 4, 64, dtype=BF, device="cuda")
+        for bad in (one[:1].expand(2, 4, 64), one[:, :1].expand(2, 4, 64)):
+            for call in (lambda: c.call(s, cache, out=bad), lambda: s.rotate(one, pos, q_out=bad),
+                         lambda: s.rotate(one, pos, k=one, k_out=bad),
+                         lambda: s.append(one[:, :2], one[:, :2], pos, slots, cache, q=one, q_out=bad)):
+                with pytest.raises(pkg.InjectError) as e:
+                    call()
+                assert e.value.status == pkg.IS_ERR_INVALID_ARG
+            # as inputs they repeat
+            a, b = s.rotate(bad, pos)[0], s.rotate(bad.contiguous(), pos)[0]
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- together
 
 def test_a_serving_step_and_its_graph(pkg):
