@@ -25,10 +25,12 @@ struct AttendArgs {
   int32_t splits_log2;         // cluster of 1, 2, 4 or 8
   // Parts of the rows' sums in the work space, each [num_tokens][num_heads]:
   // (maximum, sum) pairs and [D] sums of values, all fp32.  attend_tiles
-  // writes part `split`; attend_rows reads `num_parts` of them.
+  // writes part `split`, attend_rows with key_parts > 1 one for each of them;
+  // attend_rows and join_parts read num_parts of them.
   float2* part_ml;
   float* part_o;
   int32_t num_parts;
+  int32_t key_parts;           // attend_rows: clusters that share a unit's keys
   int32_t first_key;           // attend_rows: the keys below are in the parts
   int32_t table_shared;        // positions below are looked up in shared_blocks
   // Keys of one tensor-map box (a power of two that divides the block size and

@@ -20,12 +20,13 @@
 // next bring keys and values, as TMA boxes of a block's tokens, into a ring
 // of up to 192 KB; one thread of the last warp issues the products, the next
 // tile's scores ahead of this tile's sums.  The keys of a unit can be split
-// over a cluster, whose CTAs join their sums through distributed shared memory.
+// over a cluster, whose CTAs join their sums through distributed shared memory,
+// and long ones over several clusters, whose sums a grid behind joins.
 //
 // Measured on B200 (32 query and 8 KV heads of 128, block 16): 100 requests of
 // 800-3200 keys 141 us, 5.8 TB/s of keys and values, 0.90 of the copy
-// bandwidth; 3 requests of 60-131 k keys (4 KV heads, clusters of 8: 96 of 148
-// SMs) 126 us, 5.0 TB/s.  A tile costs an SM some 1500 cycles, of 2200 that its
+// bandwidth; 3 requests of 60-131 k keys (4 KV heads, 12 parts: 144 of 148 SMs)
+// 114 us, 5.5 TB/s, as the longest one's parts end last.  A tile costs an SM some 1500 cycles, of 2200 that its
 // share of the bandwidth leaves; a unit's start and end cost some 10 000, which
 // is what bounds requests of a few hundred keys (100 of 550: 70 us, 3.3 TB/s).
 #pragma once
@@ -72,10 +73,12 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   __shared__ int32_t s_failed, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
 
-  // grid: x (KV head, split), the splits of a unit and head a cluster; y and z
-  // the unit, of which the one after the last checks the batch
+  // grid: x (KV head, part, split), the splits of a unit, head and part a
+  // cluster; y and z the unit, of which the one after the last checks the batch
+  if (a.key_parts > 1) let_next_start();
   const int32_t split = int32_t(blockIdx.x) & (a.splits - 1);
-  const int32_t h = int32_t(blockIdx.x >> a.splits_log2);
+  const int32_t h = int32_t(blockIdx.x >> a.splits_log2) / a.key_parts;
+  const int32_t part = int32_t(blockIdx.x >> a.splits_log2) - h * a.key_parts;
   const int64_t unit = int64_t(blockIdx.z) * gridDim.y + blockIdx.y;
   if (unit >= a.units) {
     if (unit == a.units && blockIdx.x == 0) check_requests<NT>(a);
@@ -120,10 +123,12 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   // tiles, from a box's border on (the keys below first_key are left out)
   const int32_t begin = a.box_log2 < 0 ? a.first_key : a.first_key >> a.box_log2 << a.box_log2;
   const int32_t end = row_limit(a, rq, token_of(rows - 1));
-  const int32_t all_tiles = end > a.first_key ? int32_t(uint32_t(end - begin + kTileKeys - 1) / kTileKeys) : 0;
-  const int32_t lo = begin + (all_tiles * split >> a.splits_log2) * kTileKeys;
-  const int32_t last = all_tiles * (split + 1) >> a.splits_log2;
-  const int32_t hi = all_tiles == 0 ? lo : last == all_tiles ? end : begin + last * kTileKeys;
+  const uint32_t all_tiles = end > a.first_key ? uint32_t(end - begin + kTileKeys - 1) / kTileKeys : 0;
+  const uint32_t shares = a.key_parts << a.splits_log2, mine = (part << a.splits_log2) + split;
+  // (up to 2^24 tiles, times fewer than 2^8 shares)
+  const int32_t lo = begin + int32_t(all_tiles * mine / shares) * kTileKeys;
+  const uint32_t last = all_tiles * (mine + 1) / shares;
+  const int32_t hi = all_tiles == 0 ? lo : last == all_tiles ? end : begin + int32_t(last) * kTileKeys;
   const int32_t tiles = hi > lo ? (hi - lo + kTileKeys - 1) / kTileKeys : 0;
 
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -436,6 +441,12 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
       sum.y = fmaf(w, v.y, sum.y);
       sum.z = fmaf(w, v.z, sum.z);
       sum.w = fmaf(w, v.w, sum.w);
+    }
+    if (a.key_parts > 1) {
+      const int64_t at = part * part_rows + part_row;
+      *reinterpret_cast<float4*>(a.part_o + at * D + d) = sum;
+      if (d == 0) a.part_ml[at] = make_float2(m, l);
+      continue;
     }
     // a sum of 0: no key was seen, or none with a score above -inf
     const bool none = l == 0.f;

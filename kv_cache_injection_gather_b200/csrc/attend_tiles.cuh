@@ -562,8 +562,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   }
 }
 
-// The output of rows whose sums are in parts: one warp a row.  Rows that no
-// request owns, or a refused one, are left as they are.
+// The output of rows whose sums are in parts (of either attention kernel): one
+// warp a row, the parts' weights a lane each.  Rows that no request owns, or a
+// refused one, are left as they are.  It is a launch and two dependent loads:
+// some 4 us behind the grid that writes the parts.
 constexpr int kJoinRows = 8;  // of a CTA
 
 template <int D>
@@ -577,21 +579,25 @@ __global__ void __launch_bounds__(kJoinRows * 32) join_parts_kernel(const __grid
       row < part_rows && read_request(a, owner_of(a, t), q) == 0 && t >= q.tok0 && t < q.tok0 + q.n;
   wait_for_previous();
   if (!owned) return;
-  float m = neg_inf();
-  for (int k = 0; k < a.num_parts; ++k) m = fmaxf(m, __ldcg(&a.part_ml[k * part_rows + row].x));
-  const float ref = m == neg_inf() ? 0.f : m;
-  float l = 0.f, x[D / 32] = {};
+  // lane k: part k's maximum and sum, then its weight
+  float2 ml = make_float2(neg_inf(), 0.f);
+  if (lane < a.num_parts) ml = __ldcg(&a.part_ml[lane * part_rows + row]);
+  const float m = warp_max(ml.x);
+  const float weight = exp2f(ml.x - (m == neg_inf() ? 0.f : m));
+  float l = weight * ml.y, x[D / 32] = {};
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll 8
   for (int k = 0; k < a.num_parts; ++k) {
-    const float2 ml = __ldcg(&a.part_ml[k * part_rows + row]);
-    if (ml.y == 0.f) continue;  // nothing seen: the part's values mean nothing
-    const float w = exp2f(ml.x - ref);
-    l += w * ml.y;
+    const float w = __shfl_sync(0xffffffffu, weight, k);
+    // nothing seen: the part's values mean nothing
+    const bool seen = __shfl_sync(0xffffffffu, ml.y, k) != 0.f;
     const float* o = a.part_o + (k * part_rows + row) * D;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const float2 v = __ldcg(reinterpret_cast<const float2*>(o + 64 * i + 2 * lane));
-      x[2 * i] = fmaf(w, v.x, x[2 * i]);
-      x[2 * i + 1] = fmaf(w, v.y, x[2 * i + 1]);
+      x[2 * i] = fmaf(w, seen ? v.x : 0.f, x[2 * i]);
+      x[2 * i + 1] = fmaf(w, seen ? v.y : 0.f, x[2 * i + 1]);
     }
   }
   // a sum of 0: no key was seen, or none with a score above -inf

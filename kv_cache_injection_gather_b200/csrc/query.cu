@@ -18,6 +18,7 @@
 struct is_query {
   int device = 0;
   int sm_count = 148;
+  int64_t clusters[4] = {};  // of 2^i CTAs of attend_rows that run at once
   int32_t num_layers = 0, kv_heads = 0, head_dim = 0, style = 0;
   double* turns = nullptr;  // [head_dim / 2] RoPE frequencies over 2 pi
   isq::Status* status = nullptr;
@@ -101,7 +102,14 @@ AttendKernel attend_tiles_of(int D, bool shared) {
 }
 // What joins its parts.
 using JoinKernel = void (*)(isq::AttendArgs);
-JoinKernel join_parts_of(int D) { return D == 64 ? &isq::join_parts_kernel<64> : &isq::join_parts_kernel<128>; }
+JoinKernel join_parts_of(int D) {
+  switch (D) {
+    case 64: return &isq::join_parts_kernel<64>;
+    case 128: return &isq::join_parts_kernel<128>;
+    case 256: return &isq::join_parts_kernel<256>;
+    default: return nullptr;
+  }
+}
 
 // Rows of a KV head and request up to which attend_rows takes them where
 // attend_tiles could (64 requests of 2250 keys: 32 rows take 164 us against 139,
@@ -110,6 +118,12 @@ constexpr int kMostNarrowRows = 16;
 // Keys that a split of a unit's keys should at least have, and a part.
 constexpr int kKeysPerSplit = 128;
 constexpr int kKeysPerPart = 512;
+constexpr int kKeysPerRowPart = 256;
+// Parts of attend_rows cost a grid more, some 4 us: taken where they spare a
+// CTA this many keys of a cluster's split, more where the clusters are
+// enough CTAs to fill the memory's bandwidth.
+constexpr int kKeysSpared = 1536;
+constexpr int kKeysSparedFull = 3000;
 // The shared prefix gets a grid of its own (attend_tiles over all requests'
 // rows) where the requests would otherwise read this many bytes of it.
 constexpr int64_t kSharedBytes = 64 << 20;
@@ -118,7 +132,8 @@ constexpr int64_t kSharedBytes = 64 << 20;
 // (100 requests of 2000 keys behind 4096 shared: 171 us; with parts of 2 tiles,
 // which take every SM first, 187; of 16, which end last, 192).
 constexpr int kTilesPerPart = 8;
-constexpr int kMostParts = 16;
+constexpr int kMostPrefixParts = 16;
+constexpr int kMostParts = 32;  // a lane each in join_parts
 
 // What an attention call launches; all from the host's numbers.
 struct AttendPlan {
@@ -127,6 +142,7 @@ struct AttendPlan {
   AttendKernel kernel;   // of the requests
   int64_t units;         // of the requests' grid
   int32_t splits;        // of attend_rows (a cluster)
+  int32_t key_parts;     // of attend_rows, that a grid behind joins; 1: none
   int32_t parts;         // that attend_tiles writes: of the prefix, or of the requests; 0: none
   int64_t shared_units;
   int64_t ml_bytes, o_bytes;  // work space
@@ -148,7 +164,7 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
   // a partial unit per request more than the rows fill
   p.units = most <= unit_rows ? a->num_requests : (rows + unit_rows - 1) / unit_rows + a->num_requests;
   const int64_t ctas = p.units * q->kv_heads;
-  p.splits = 1;
+  p.splits = p.key_parts = 1;
   if (p.wide) {
     // few CTAs: the keys of each in parts, that a grid behind joins
     const int64_t most_parts = std::min<int64_t>({q->sm_count / ctas, keys / kKeysPerPart, kMostParts});
@@ -161,16 +177,27 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
       const int64_t most_parts = q->sm_count / (p.shared_units * q->kv_heads);
       const int64_t tiles = (int64_t(a->shared_len) + isq::kTileKeys - 1) / isq::kTileKeys;
       p.parts = int32_t(std::max<int64_t>(
-          1, std::min<int64_t>({most_parts, (tiles + kTilesPerPart - 1) / kTilesPerPart, kMostParts})));
+          1, std::min<int64_t>({most_parts, (tiles + kTilesPerPart - 1) / kTilesPerPart, kMostPrefixParts})));
     }
-    // The keys of a unit are split over a cluster while all splits fit the SMs
-    // at once (a CTA has one to itself and costs some 10 000 cycles of start
-    // and end: 10 requests of 2250 keys take 31 us so, and 41 with twice the
-    // CTAs).
+    // The keys of a unit are split over a cluster while all clusters run at
+    // once (a CTA has an SM to itself and costs some 10 000 cycles of start and
+    // end: 10 requests of 2250 keys take 31 us so, and 41 with twice the CTAs).
     const int64_t own = keys - (p.shared ? a->shared_len : 0);
-    while (p.splits < isq::kMostSplits && ctas * p.splits * 2 <= q->sm_count &&
-           own >= int64_t(2 * p.splits) * kKeysPerSplit)
-      p.splits *= 2;
+    for (int i = 1; (1 << i) <= isq::kMostSplits && ctas <= q->clusters[i] && own >= (kKeysPerSplit << i); ++i)
+      p.splits = 1 << i;
+    // Few units of many keys: shares for every SM, in clusters as small as
+    // kMostParts allows (larger ones leave SMs unused), whose sums are parts
+    // that a grid behind joins.  One decoding request of 131 k keys, 8 KV heads:
+    // 117 us in clusters, 94 so; 1 KV head: 116 and 25; of 16 k keys, 8 heads: 25
+    // and 27.
+    const int64_t shares = std::min<int64_t>(q->sm_count / ctas, own / kKeysPerRowPart);
+    const bool full = ctas * p.splits * 8 > int64_t(q->sm_count) * 5;
+    if (!p.shared && shares > p.splits && join_parts_of(q->head_dim) &&
+        own / p.splits - own / shares >= (full ? kKeysSparedFull : kKeysSpared)) {
+      const int i = shares > 3 * kMostParts ? 2 : shares > kMostParts ? 1 : 0;
+      p.splits = 1 << i;
+      p.parts = p.key_parts = int32_t(std::min<int64_t>({kMostParts, shares >> i, q->clusters[i] / ctas}));
+    }
   }
   if (p.parts) {
     const int64_t part_rows = int64_t(p.parts) * a->num_tokens * a->q.num_heads;
@@ -305,11 +332,28 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
   for (bool norm : {false, true})
     ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(
                                                 rows_kernel_of(c.head_dim, c.rope_style, norm))) == cudaSuccess;
-  ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(join_parts_of(c.head_dim))) == cudaSuccess;
+  if (join_parts_of(c.head_dim))
+    ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(join_parts_of(c.head_dim))) == cudaSuccess;
   for (const AttendKernel& k : {attend_rows_of(c.head_dim, 16), attend_rows_of(c.head_dim, 32),
                                 attend_tiles_of(c.head_dim, false), attend_tiles_of(c.head_dim, true)})
     ok = ok && (!k.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) == cudaSuccess);
+  // Clusters that run at once: one CTA an SM, but a cluster's in one GPC.
+  for (int i = 0; i < 4 && ok; ++i) {
+    const AttendKernel k = attend_rows_of(c.head_dim, 16);
+    cudaLaunchAttribute size{};
+    size.id = cudaLaunchAttributeClusterDimension;
+    size.val.clusterDim = {1u << i, 1, 1};
+    cudaLaunchConfig_t one{};
+    one.gridDim = dim3(1u << i);
+    one.blockDim = dim3(unsigned(k.threads));
+    one.dynamicSmemBytes = size_t(k.smem);
+    one.attrs = &size;
+    one.numAttrs = 1;
+    int n = 0;
+    ok = cudaOccupancyMaxActiveClusters(&n, k.fn, &one) == cudaSuccess && n > 0;
+    q->clusters[i] = n;
+  }
   void* encode = nullptr;
   cudaDriverEntryPointQueryResult found{};
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &encode, 12000, cudaEnableDefault, &found) ==
@@ -439,7 +483,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   }
   // attend_tiles: one dimension; attend_rows: (head, split), units, more units
   const int64_t shared_grid = p.shared_units * query->kv_heads * p.parts;
-  const int64_t grid_x = p.wide ? p.units * query->kv_heads * std::max(1, p.parts) + 1 : int64_t(query->kv_heads) * p.splits;
+  const int64_t grid_x = p.wide ? p.units * query->kv_heads * std::max(1, p.parts) + 1 : int64_t(query->kv_heads) * p.key_parts * p.splits;
   const int64_t grid_y = p.wide ? 1 : std::min<int64_t>(p.units + 1, 32768);
   const int64_t grid_z = p.wide ? 1 : (p.units + grid_y) / grid_y;
   if (grid_x > INT32_MAX || shared_grid > INT32_MAX || grid_z > 65535) return IS_ERR_CAPACITY;
@@ -506,14 +550,16 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   }
   a.units = p.units;
   a.splits = p.wide ? std::max(1, p.parts) : p.splits;
+  a.key_parts = p.key_parts;
   if (!p.wide && p.splits > 1) {
     while ((1 << a.splits_log2) < p.splits) ++a.splits_log2;
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.splits), 1, 1};
   }
   ok = ok && launch(p.kernel, dim3(unsigned(grid_x), unsigned(grid_y), unsigned(grid_z)));
-  if (p.wide && p.parts) {
+  if (p.parts && !p.shared) {
     a.num_parts = p.parts;
+    cfg.numAttrs = 0;
     beside();
     const int64_t rows = int64_t(a.num_tokens) * a.num_heads;
     cfg.gridDim = dim3(unsigned((rows + isq::kJoinRows - 1) / isq::kJoinRows));

@@ -606,6 +606,54 @@ def test_attend_host_refusals(pkg):
             s.append(x[:, :2], x[:, :2], c.i32([0, 1]), torch.zeros(2, dtype=torch.int64, device="cuda"), cache, 5)
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("n,mem,H,G,shared", [([1], [40001], 1, 4, 0), ([1, 3, 0, 1], [26000, 10, 7, 0], 1, 5, 37),
+                                              ([2, 1], [17000, 33000], 2, 7, 0)])
+def test_attend_keys_in_parts(pkg, D, n, mem, H, G, shared):
+    """Few units of many keys: parts of the keys that a second grid joins, of
+    which short requests leave most empty."""
+    c = Paged(94, D, H, G, 16, n, mem, shared=shared, extra_rows=2)
+    check_attend(pkg, c)
+    c = Paged(95, D, H, G, 24, n, mem, shared=shared, head_major=True)
+    check_attend(pkg, c, causal=False, scale=0.2)
+
+
+def test_keys_in_parts_in_a_graph_with_bad_and_masked_blocks(pkg):
+    H, G, D, B = 1, 4, 128, 16
+    c = Paged(96, D, H, G, B, [2, 1], [30000, 20011])
+    with make(pkg, D, H) as s:
+        cache = pkg.cache_desc(c.k_cache, c.v_cache)
+        clean = c.call(s, cache)
+        assert s.last_query_error() == (0, 0)
+        # the last key, which only the request's last query sees
+        for x in (c.k_cache, c.v_cache):
+            x[c.layer, int(c.tables[0, (c.kv[0] - 1) // B]), (c.kv[0] - 1) % B] = math.inf
+        ref, _, tol = c.reference()
+        within(c.call(s, cache)[:1], ref[:1], tol[:1])
+        c.sync_cache()
+        # a bad block's keys are left out
+        t = c.tables
+        c.tables = t.clone()
+        c.tables[1, 900] = c.k_cache.shape[1]
+        bad = c.call(s, cache)
+        assert s.last_query_error() == (pkg.IS_ERR_BAD_BLOCK, 1)
+        assert torch.equal(bad[:2], clean[:2]) and torch.isfinite(bad).all() and not torch.equal(bad, clean)
+        c.tables = t
+        # in place, captured and replayed
+        q0 = c.q.clone()
+        ints = [c.i32(x) for x in (c.q_off, c.start, c.kv)]
+        tables = c.tables.cuda()
+        run = lambda: s.attend(c.q, *ints, tables, cache, c.layer, max_q_len=2, out=c.q)  # noqa: E731
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(3):
+            c.q.copy_(q0)
+            graph.replay()
+            assert torch.equal(c.q, clean)
+        assert s.last_query_error() == (0, 0)
+
+
 @pytest.mark.parametrize("n,R,shared", [(1, 3, 0), (70, 3, 0), (1, 64, 3000)])
 def test_attend_scores_all_minus_infinity(pkg, n, R, shared):
     """Rows whose every score is -inf get zeros, as rows that see no key."""
