@@ -31,13 +31,16 @@
 // 4096 tokens 280-310 us (870-960 TFLOP/s, 0.52-0.57 of the burst bf16 GEMM;
 // the spread is the card's power limit), 100 requests of 16-64 queries over
 // 3300-5000 keys 385 us (690 TFLOP/s of what is not masked or padded); with a
-// tile as one piece 303-328 and 412 us.  The products of a tile of both streams
-// take 2300 cycles (their operands' shared-memory reads; at 128 x 128 x 16 both
-// sides are read for 64 cycles of work), its exponentials 2048 on the
-// special-function units less the share below, with the loads, the maximum and
-// the conversions beside them on the same warps: two streams do not hide all of
-// that, and a third does not fit the tensor memory.  A unit's start and end
-// cost 15 000 cycles, of some 60 000 for 4096 keys.
+// tile as one piece 303-328 and 412 us.  A tile of both streams takes 3400
+// cycles.  Its halves alternate between softmax (maximum 300, exponentials
+// 1100, 770 of which the special-function units take for both streams) and
+// products (both streams' 1300, as scores of 64 keys read more shared memory
+// than they compute on, and 350 from the last probability to the first
+// product and from the last product to the next maximum): the two phases are
+// equally long, and neither waits for the other alone.  Products in strict turns,
+// from two threads or one, shorten the softmax to 1050 but idle between turns:
+// the same 3400.  A unit's start costs 8200 cycles (its queries arrive at 6600),
+// its end 6600 and the next CTA 1300, of some 60 000 for 4096 keys.
 #pragma once
 
 #include "attend_common.cuh"
@@ -271,13 +274,15 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         tc_commit(&bar_empty[at]);
         if (!by_rows) tc_commit(&bar_empty[at]);
       };
-      // scores of half a tile, its 64 keys from 64 * half on
+      // scores of half a tile, its 64 keys from 64 * half on (descriptors count
+      // in 16 bytes: a step along a tile is an addition)
       auto scores = [&](int at, int half) {
         tc_fence_after();
         const uint32_t ka = ring_at + at * S::kSlotBytes + half * (S::kSlotBytes / 2);
+        const uint64_t qd = operand<D>(qa, 16), kd = operand<D>(ka, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(ts + half * 64, operand<D>(qa + dims_at<D>(k), 16), operand<D>(ka + dims_at<D>(k), 16),
+          mma_ss(ts + half * 64, qd + (dims_at<D>(k) >> 4), kd + (dims_at<D>(k) >> 4),
                  product(kTileKeys / 2, false, false), k > 0);
         tc_commit(&bar_s[st][half]);
         if (half == 1) free_slot(at);
@@ -299,10 +304,11 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
           ok = ok && bar_wait(&bar_p[st][half], i & 1, &s_failed);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t vd = operand<D>(va + half * (D * 128), kSlabStep);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(to, ts + half * 64 + k * 8, operand<D>(va + (4 * half + k) * (D * 32), kSlabStep),
-                   product(D, false, true), i > 0 || half > 0 || k > 0);
+            mma_ts(to, ts + half * 64 + k * 8, vd + k * (D * 32 / 16), product(D, false, true),
+                   i > 0 || half > 0 || k > 0);
           tc_commit(&bar_o[st][half]);
           if (half == 1) free_slot(slot + 1);
           // (the next scores overwrite the probabilities that these products
