@@ -26,9 +26,10 @@
 // Measured on B200 (32 query and 8 KV heads of 128, block 16): 100 requests of
 // 800-3200 keys 141 us, 5.8 TB/s of keys and values, 0.90 of the copy
 // bandwidth; 3 requests of 60-131 k keys (4 KV heads, 12 parts: 144 of 148 SMs)
-// 114 us, 5.5 TB/s, as the longest one's parts end last.  A tile costs an SM some 1500 cycles, of 2200 that its
-// share of the bandwidth leaves; a unit's start and end cost some 10 000, which
-// is what bounds requests of a few hundred keys (100 of 550: 70 us, 3.3 TB/s).
+// 114 us, 5.5 TB/s, as the longest one's parts end last.  A tile costs an SM
+// some 1500 cycles, of 2200 that its share of the bandwidth leaves; a unit's
+// start and end cost some 10 000, which is what bounds requests of a few hundred
+// keys (100 of 550: 70 us, 3.3 TB/s).
 #pragma once
 
 #include "attend_common.cuh"

@@ -1,6 +1,6 @@
 // Host side of the query calls declared in include/inject_query.h: the
 // handle, the checks of arguments and the launches of the kernels in
-// query_rows.cuh and attend_rows.cuh.
+// query_rows.cuh, attend_rows.cuh and attend_tiles.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -100,7 +100,7 @@ AttendKernel attend_tiles_of(int D, bool shared) {
   if (D == 128) return attend_tiles_of<128>(shared);
   return {nullptr, 0, 0, 0};
 }
-// What joins its parts.
+// What joins parts, of either kernel (head_dim 32 has none).
 using JoinKernel = void (*)(isq::AttendArgs);
 JoinKernel join_parts_of(int D) {
   switch (D) {
@@ -143,7 +143,7 @@ struct AttendPlan {
   int64_t units;         // of the requests' grid
   int32_t splits;        // of attend_rows (a cluster)
   int32_t key_parts;     // of attend_rows, that a grid behind joins; 1: none
-  int32_t parts;         // that attend_tiles writes: of the prefix, or of the requests; 0: none
+  int32_t parts;         // in the work space: of the prefix, or of the requests' keys; 0: none
   int64_t shared_units;
   int64_t ml_bytes, o_bytes;  // work space
 };
@@ -195,8 +195,11 @@ AttendPlan plan_attend(const is_query* q, const is_attend_t* a, const is_cache_t
     if (!p.shared && shares > p.splits && join_parts_of(q->head_dim) &&
         own / p.splits - own / shares >= (full ? kKeysSparedFull : kKeysSpared)) {
       const int i = shares > 3 * kMostParts ? 2 : shares > kMostParts ? 1 : 0;
-      p.splits = 1 << i;
-      p.parts = p.key_parts = int32_t(std::min<int64_t>({kMostParts, shares >> i, q->clusters[i] / ctas}));
+      const int64_t parts = std::min<int64_t>({kMostParts, shares >> i, q->clusters[i] / ctas});
+      if (parts > 1) {
+        p.splits = 1 << i;
+        p.parts = p.key_parts = int32_t(parts);
+      }
     }
   }
   if (p.parts) {
@@ -280,8 +283,8 @@ int check_attend(const is_query* q, const is_attend_t* a, const is_cache_t* c) {
   if (a->q.num_heads <= 0 || a->q.num_heads % q->kv_heads != 0 || a->out.num_heads != a->q.num_heads)
     return IS_ERR_INVALID_ARG;
   if (a->num_tokens > 0 && a->num_requests > 0) {
-    if (!rows_ok(&a->q) || !out_ok(&a->out, a->num_tokens) || !a->q_offsets || !a->start_pos || !a->kv_lens || a->max_q_len < 1 ||
-        (a->max_blocks_per_req > 0 && !a->block_tables) || (a->shared_len > 0 && !a->shared_blocks))
+    if (!rows_ok(&a->q) || !out_ok(&a->out, a->num_tokens) || !a->q_offsets || !a->start_pos || !a->kv_lens ||
+        a->max_q_len < 1 || (a->max_blocks_per_req > 0 && !a->block_tables) || (a->shared_len > 0 && !a->shared_blocks))
       return IS_ERR_INVALID_ARG;
   }
   if (int64_t(a->num_tokens) * a->q.num_heads > INT32_MAX || a->shared_len > isq::kMostKeys) return IS_ERR_CAPACITY;
@@ -396,8 +399,8 @@ int is_query_rotate(is_query_t* query, int32_t num_tokens, const int32_t* positi
                     const void* k_weight, float eps, void* stream) {
   if (!query || num_tokens < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return IS_ERR_INVALID_ARG;
   if (num_tokens == 0) return IS_OK;
-  if (!positions || !rows_ok(q) || !out_ok(q_out, num_tokens) || q->num_heads != q_out->num_heads || !aligned16(q_weight) ||
-      !aligned16(k_weight) || (k == nullptr) != (k_out == nullptr))
+  if (!positions || !rows_ok(q) || !out_ok(q_out, num_tokens) || q->num_heads != q_out->num_heads ||
+      !aligned16(q_weight) || !aligned16(k_weight) || (k == nullptr) != (k_out == nullptr))
     return IS_ERR_INVALID_ARG;
   if (k && (!rows_ok(k) || !out_ok(k_out, num_tokens) || k->num_heads != k_out->num_heads)) return IS_ERR_INVALID_ARG;
   OnDevice guard(query->device);
@@ -483,7 +486,8 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
   }
   // attend_tiles: one dimension; attend_rows: (head, split), units, more units
   const int64_t shared_grid = p.shared_units * query->kv_heads * p.parts;
-  const int64_t grid_x = p.wide ? p.units * query->kv_heads * std::max(1, p.parts) + 1 : int64_t(query->kv_heads) * p.key_parts * p.splits;
+  const int64_t grid_x = query->kv_heads * (p.wide ? p.units * std::max(1, p.parts) : int64_t(p.key_parts) * p.splits) +
+                         (p.wide ? 1 : 0);
   const int64_t grid_y = p.wide ? 1 : std::min<int64_t>(p.units + 1, 32768);
   const int64_t grid_z = p.wide ? 1 : (p.units + grid_y) / grid_y;
   if (grid_x > INT32_MAX || shared_grid > INT32_MAX || grid_z > 65535) return IS_ERR_CAPACITY;
