@@ -192,10 +192,13 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
         tc_commit(&bar_empty[slot]);
         tc_commit(&bar_o);
       }
-      if (!ok) {  // the products in flight
-        tc_commit(&bar_end);
-        bar_wait(&bar_end, 0, nullptr);
-      }
+      // All products are done before the threads meet: O is read then, and the
+      // CTA may leave.  (bar_o cannot say so.  A parity tells phase n from n - 1
+      // and n + 1, so a wait for n counts only where n - 1 is known to be done;
+      // the last scores are issued ahead of the last but one sums, whose phase
+      // nothing waits for.)
+      tc_commit(&bar_end);
+      if (!bar_wait(&bar_end, 0, nullptr)) s_failed = 1;
     }
     __syncwarp();
   } else {
@@ -277,8 +280,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
           s_shrink[tid] = top == neg_inf() ? 1.f : exp2_fast(old - top);
         }
         asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-        // (the sums up to t - 2 are done: their commit came before that of this
-        // tile's scores)
+        // (the sums up to t - 2 are done, as a wait for phase t - 1 needs: their
+        // commit came before that of this tile's scores)
         if (t > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(&bar_o, (t - 1) & 1, &s_failed));
         if (t > 0 && ok) {
           tc_fence_after();
@@ -332,7 +335,6 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
         for (int i = 0; i < 4; ++i) l[c + i] += __shfl_xor_sync(0xffffffffu, l[c + i], d);
       if (lane == 0) *reinterpret_cast<float4*>(&s_top[warp][c]) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
     }
-    if (tiles > 0) bar_wait(&bar_o, (tiles - 1) & 1, &s_failed);
     __syncwarp();
   }
   tc_fence_before();
