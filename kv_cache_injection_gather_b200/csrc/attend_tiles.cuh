@@ -94,11 +94,13 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
 // 2^x of two values up to 2^7 without the special-function unit: x = n + f with
 // n whole and |f| <= 1/2, 2^f by a polynomial of degree 4 (the coefficients
 // minimise the largest relative error on that interval, 2.6e-6 = 2^-18.5,
-// found by reweighted least squares), n added to the exponent.  Below 2^-126
-// it stays there.  Adding 1.5 * 2^23 leaves n in a sum's low bits.
+// found by reweighted least squares), times 2^n.  Below 2^-126 it stays there.
+// Adding 1.5 * 2^23 leaves n in a sum's low bits.  A NaN stays one: it goes
+// through the polynomial and the product (n added to the exponent's bits would
+// make a NaN a large number).
 __device__ __forceinline__ Two exp2_two(Two x) {
   const float2 in = both(x);
-  float lo, hi;  // (a NaN stays one)
+  float lo, hi;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(in.x), "f"(-126.f));
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(in.y), "f"(-126.f));
   x = two(lo, hi);
@@ -110,9 +112,9 @@ __device__ __forceinline__ Two exp2_two(Two x) {
   p = fma2(p, f, two(0.240247443318367f, 0.240247443318367f));
   p = fma2(p, f, two(0.6931217908859253f, 0.6931217908859253f));
   p = fma2(p, f, two(0.9999992847442627f, 0.9999992847442627f));
-  const float2 pf = both(p), tf = both(t);
-  return two(__uint_as_float(__float_as_uint(pf.x) + (__float_as_uint(tf.x) << 23)),
-             __uint_as_float(__float_as_uint(pf.y) + (__float_as_uint(tf.y) << 23)));
+  const float2 n = both(t);  // bits of 2^n: n + 127 in the exponent
+  return mul(p, two(__uint_as_float((__float_as_uint(n.x) << 23) + 0x3f800000u),
+                    __uint_as_float((__float_as_uint(n.y) << 23) + 0x3f800000u)));
 }
 
 // The request that owns query token t: the last r with q_offsets[r] <= t.
