@@ -48,7 +48,10 @@ void is_query_destroy(is_query_t* query);
 
 /* Wait for `stream`, then return and clear the first device-side error
  * recorded since the previous call (IS_OK if none); *detail_out, if not
- * NULL, receives its index (see each call). */
+ * NULL, receives its index (see each call).  Only `stream` is waited for: an
+ * error of work that is still under way on another stream is kept for a later
+ * call, one recorded there already is returned too.  A stream that is being
+ * captured is refused (CUDA; the capture is lost). */
 int is_query_last_error(is_query_t* query, void* stream, int64_t* detail_out);
 
 /* Rows of head vectors: element (token t, head h, dim d) is

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <new>
 
 #include "attend_rows.cuh"
@@ -22,6 +23,7 @@ struct is_query {
   int32_t num_layers = 0, kv_heads = 0, head_dim = 0, style = 0;
   double* turns = nullptr;  // [head_dim / 2] RoPE frequencies over 2 pi
   isq::Status* status = nullptr;
+  std::mutex taking;         // one is_query_last_error at a time takes the status
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;  // the driver's
 };
 
@@ -331,7 +333,7 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
   // Attributes now, so that the calls are launches alone (the functions are
   // loaded here, not inside somebody's stream capture).
   cudaFuncAttributes attr;
-  bool ok = true;
+  bool ok = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(&isq::take_status_kernel)) == cudaSuccess;
   for (bool norm : {false, true})
     ok = ok && cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(
                                                 rows_kernel_of(c.head_dim, c.rope_style, norm))) == cudaSuccess;
@@ -385,13 +387,19 @@ void is_query_destroy(is_query_t* q) {
 int is_query_last_error(is_query_t* q, void* stream, int64_t* detail) {
   if (!q) return IS_ERR_INVALID_ARG;
   OnDevice guard(q->device);
-  isq::Status s{};
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-      cudaMemcpy(&s, q->status, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess)
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Its work is done first, so that nothing is waited for under the lock (and
+  // a stream that is being captured is refused before a launch).
+  if (cudaStreamSynchronize(st) != cudaSuccess) return IS_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(q->taking);
+  unsigned long long word = 0;
+  isq::take_status_kernel<<<1, 1, 0, st>>>(q->status);
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&word, &q->status->taken, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return IS_ERR_CUDA;
-  if (s.code != 0 && cudaMemset(q->status, 0, sizeof(s)) != cudaSuccess) return IS_ERR_CUDA;
-  if (detail) *detail = s.detail;
-  return s.code;
+  if (detail) *detail = int32_t(uint32_t(word));
+  return int32_t(uint32_t(word >> 32));
 }
 
 int is_query_rotate(is_query_t* query, int32_t num_tokens, const int32_t* positions, const is_rows_t* q,

@@ -26,16 +26,20 @@ enum : int32_t {
   kErrTimeout = -8,
 };
 
+// The first error since the last one was taken, in one word so that its code
+// and detail arrive and leave together: code in the upper half (0: none),
+// detail in the lower.
 struct Status {
-  int32_t code;
-  int32_t pad;
-  long long detail;
+  unsigned long long first;
+  unsigned long long taken;  // for the host
 };
 
-// The first error is kept.
-__device__ __forceinline__ void record(Status* st, int32_t code, long long detail) {
-  if (atomicCAS(&st->code, 0, code) == 0) st->detail = detail;
+__device__ __forceinline__ void record(Status* st, int32_t code, int32_t detail) {
+  atomicCAS(&st->first, 0ull, (static_cast<unsigned long long>(static_cast<uint32_t>(code)) << 32) | uint32_t(detail));
 }
+
+// Takes the error in the order of the stream that it is launched on.
+__global__ void take_status_kernel(Status* st) { st->taken = atomicExch(&st->first, 0ull); }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     to[2] = v2.y;
   }
   if (append && (slot < -1 || slot >= a.num_slots)) {
-    if (tid == 0) record(a.st, kErrBadBlock, t);
+    if (tid == 0) record(a.st, kErrBadBlock, int32_t(t));
     slot = -1;
   }
   __syncthreads();
