@@ -48,6 +48,22 @@ void free_query(is_query* q) {
   delete q;
 }
 
+// A failed runtime call's error is this call's: no later one finds it.
+int cuda_error() {
+  cudaGetLastError();
+  return IS_ERR_CUDA;
+}
+
+// Launches; whether that worked is said by the launch alone.
+template <typename... Args>
+bool start(void (*fn)(Args...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Kernel tables over head_dim and its variants.
@@ -271,8 +287,7 @@ int launch_rows(const is_query* q, const isq::RowArgs& a, int32_t num_tokens, cu
   const int most = num_tokens < 4 * q->sm_count ? isq::kRowThreads : 64;
   const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
   const unsigned threads = unsigned(std::min<int64_t>(want, most));
-  rows_kernel_of(q->head_dim, q->style, norm)<<<unsigned(num_tokens), threads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? IS_OK : IS_ERR_CUDA;
+  return start(rows_kernel_of(q->head_dim, q->style, norm), unsigned(num_tokens), threads, st, a) ? IS_OK : cuda_error();
 }
 
 // The arguments of an attention call that do not need the device; IS_OK, or
@@ -311,10 +326,7 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
     return IS_ERR_INVALID_ARG;
   if (!rows_kernel_of(c.head_dim, 0, false)) return IS_ERR_NOT_SUPPORTED;
   int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) {
-    cudaGetLastError();
-    return IS_ERR_CUDA;
-  }
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) return cuda_error();
   OnDevice guard(device);
   is_query* q = new (std::nothrow) is_query();
   if (!q) return IS_ERR_OOM;
@@ -366,12 +378,12 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
       found == cudaDriverEntryPointSuccess)
     q->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode);
   ok = ok && q->encode && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
-  isq::turns_kernel<<<(c.head_dim / 2 + 127) / 128, 128>>>(q->turns, c.head_dim, c.rope_theta, c.rope_scaling,
-                                                           c.scale_factor, c.low_freq_factor, c.high_freq_factor,
-                                                           double(c.original_max_position));
-  if (!ok || cudaGetLastError() != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  ok = ok && start(&isq::turns_kernel, unsigned(c.head_dim / 2 + 127) / 128, 128, nullptr, q->turns, int(c.head_dim),
+                   c.rope_theta, int(c.rope_scaling), c.scale_factor, c.low_freq_factor, c.high_freq_factor,
+                   double(c.original_max_position));
+  if (!ok || cudaDeviceSynchronize() != cudaSuccess) {
     free_query(q);
-    return IS_ERR_CUDA;
+    return cuda_error();
   }
   *out = q;
   return IS_OK;
@@ -390,14 +402,13 @@ int is_query_last_error(is_query_t* q, void* stream, int64_t* detail) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Its work is done first, so that nothing is waited for under the lock (and
   // a stream that is being captured is refused before a launch).
-  if (cudaStreamSynchronize(st) != cudaSuccess) return IS_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return cuda_error();
   std::lock_guard<std::mutex> lock(q->taking);
   unsigned long long word = 0;
-  isq::take_status_kernel<<<1, 1, 0, st>>>(q->status);
-  if (cudaGetLastError() != cudaSuccess ||
+  if (!start(&isq::take_status_kernel, 1, 1, st, q->status) ||
       cudaMemcpyAsync(&word, &q->status->taken, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
-    return IS_ERR_CUDA;
+    return cuda_error();
   if (detail) *detail = int32_t(uint32_t(word));
   return int32_t(uint32_t(word >> 32));
 }
@@ -579,11 +590,7 @@ int is_query_attend(is_query_t* query, const is_attend_t* args, const is_cache_t
     cfg.dynamicSmemBytes = 0;
     ok = ok && cudaLaunchKernelEx(&cfg, join_parts_of(query->head_dim), a) == cudaSuccess;
   }
-  if (!ok) {
-    cudaGetLastError();
-    return IS_ERR_CUDA;
-  }
-  return IS_OK;
+  return ok ? IS_OK : cuda_error();
 }
 
 }  // extern "C"

@@ -1,5 +1,7 @@
 """last_query_error: the first error since the last call, taken in the order of
 the stream that it is given, whatever other streams are doing."""
+import ctypes
+
 import pytest
 import torch
 
@@ -75,3 +77,21 @@ def test_the_first_of_many_is_kept_whole(pkg):  # noqa: F811
             s.last_query_error()
         assert s.last_query_error() == (0, 0)
 
+
+def test_a_refused_wait_does_not_fail_the_next_call(pkg):  # noqa: F811
+    """Waiting for a stream that is being captured is an error of that call,
+    and of no later one."""
+    cudart = ctypes.CDLL("libcudart.so.12")
+    with make(pkg, 64, 2, layers=1) as s:
+        calls = Calls(pkg, s)
+        st = torch.cuda.Stream()
+        raw, graph = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p()
+        assert cudart.cudaStreamBeginCapture(raw, 2) == 0  # relaxed
+        assert s.last_query_error(st.cuda_stream)[0] == pkg.IS_ERR_CUDA
+        cudart.cudaStreamEndCapture(raw, ctypes.byref(graph))
+        cudart.cudaGetLastError()
+        if graph.value:
+            cudart.cudaGraphDestroy(graph)
+        q, _ = s.rotate(calls.x, calls.pos)
+        assert torch.equal(q, calls.x)
+        assert s.last_query_error() == (0, 0)
