@@ -535,8 +535,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
         a.part_ml[part_row] = make_float2(m, l);
       else if (mine && a.lse != nullptr)
         a.lse[t * a.num_heads + head] = none ? neg_inf() : (m + log2f(l)) * kLn2;
-      // odd rows, one after the other by the whole warp
+      // odd rows, one after the other by the whole warp, whose stores come
+      // behind what the rows' own threads have stored above
       uint32_t todo = __ballot_sync(0xffffffffu, odd && mine);
+      __syncwarp();
       while (todo) {
         const int from = __ffs(todo) - 1;
         todo &= todo - 1;
