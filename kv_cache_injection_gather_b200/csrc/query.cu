@@ -19,7 +19,7 @@
 struct is_query {
   int device = 0;
   int sm_count = 148;
-  int64_t clusters[4] = {};  // of 2^i CTAs of attend_rows that run at once
+  int64_t clusters[4] = {};  // of 2^i CTAs of attend_rows that run at once; 0: none of this size
   int32_t num_layers = 0, kv_heads = 0, head_dim = 0, style = 0;
   double* turns = nullptr;  // [head_dim / 2] RoPE frequencies over 2 pi
   isq::Status* status = nullptr;
@@ -153,6 +153,22 @@ constexpr int kTilesPerPart = 8;
 constexpr int kMostPrefixParts = 16;
 constexpr int kMostParts = 32;  // a lane each in join_parts
 
+// Fills in the clusters of 2^i CTAs that run at once, as ask(CTAs, number)
+// says: one CTA an SM, but a cluster's in one GPC, so a part of a GPU may have
+// room for none of the larger ones.  False where not even one CTA runs.
+template <typename Ask>
+bool count_clusters(int64_t (&clusters)[4], Ask ask) {
+  for (int i = 0; i < 4; ++i) {
+    int n = 0;
+    if (ask(1u << i, &n) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    clusters[i] = n;
+  }
+  return clusters[0] > 0;
+}
+
 // What an attention call launches; all from the host's numbers.
 struct AttendPlan {
   bool wide;             // attend_tiles over requests, else attend_rows
@@ -256,14 +272,14 @@ uint16_t* layer_of(void* cache, const is_cache_t* c, int32_t layer) {
 // 32); the head is a slab number.  A box is a head's dims x the largest power
 // of two of tokens that divides the block and a tile of keys.  Returns that
 // power's logarithm, or -1 where there is no such box: under 8 tokens, a head
-// stride between slabs, strides that a map cannot have (the kernels then
-// gather key by key).
+// stride between slabs, strides that a map cannot have, a driver that makes no
+// maps (the kernels then gather key by key).
 int box_maps(const is_query* q, isq::AttendArgs& a, CUtensorMap& k, CUtensorMap& v) {
   int box = 0;
   while ((2 << box) <= isq::kTileKeys && a.block_size % (2 << box) == 0) ++box;
   const int D = q->head_dim, slab = std::min(D, 64);
   const int64_t slabs = (a.kv_heads - 1) * (a.head_stride / slab) + D / slab;
-  if (box < 3 || a.head_stride % slab != 0 || slabs > INT32_MAX) return -1;
+  if (!q->encode || box < 3 || a.head_stride % slab != 0 || slabs > INT32_MAX) return -1;
   a.head_slabs = int32_t(a.kv_heads > 1 ? a.head_stride / slab : 0);
   const cuuint64_t dims[5] = {cuuint64_t(slab), 8, cuuint64_t(slabs), cuuint64_t(a.block_size / 8), cuuint64_t(a.num_blocks)};
   const cuuint64_t strides[4] = {cuuint64_t(a.token_stride) * 2, cuuint64_t(slab) * 2, cuuint64_t(a.token_stride) * 16,
@@ -355,29 +371,26 @@ int is_query_create(const is_store_config_t* cfg, int device, is_query_t** out) 
                                 attend_tiles_of(c.head_dim, false), attend_tiles_of(c.head_dim, true)})
     ok = ok && (!k.fn || cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) == cudaSuccess);
-  // Clusters that run at once: one CTA an SM, but a cluster's in one GPC.
-  for (int i = 0; i < 4 && ok; ++i) {
-    const AttendKernel k = attend_rows_of(c.head_dim, 16);
-    cudaLaunchAttribute size{};
-    size.id = cudaLaunchAttributeClusterDimension;
-    size.val.clusterDim = {1u << i, 1, 1};
-    cudaLaunchConfig_t one{};
-    one.gridDim = dim3(1u << i);
-    one.blockDim = dim3(unsigned(k.threads));
-    one.dynamicSmemBytes = size_t(k.smem);
-    one.attrs = &size;
-    one.numAttrs = 1;
-    int n = 0;
-    ok = cudaOccupancyMaxActiveClusters(&n, k.fn, &one) == cudaSuccess && n > 0;
-    q->clusters[i] = n;
-  }
+  ok = ok && count_clusters(q->clusters, [&](unsigned ctas, int* n) {
+         const AttendKernel k = attend_rows_of(c.head_dim, 16);
+         cudaLaunchAttribute size{};
+         size.id = cudaLaunchAttributeClusterDimension;
+         size.val.clusterDim = {ctas, 1, 1};
+         cudaLaunchConfig_t one{};
+         one.gridDim = dim3(ctas);
+         one.blockDim = dim3(unsigned(k.threads));
+         one.dynamicSmemBytes = size_t(k.smem);
+         one.attrs = &size;
+         one.numAttrs = 1;
+         return cudaOccupancyMaxActiveClusters(n, k.fn, &one);
+       });
   void* encode = nullptr;
   cudaDriverEntryPointQueryResult found{};
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &encode, 12000, cudaEnableDefault, &found) ==
           cudaSuccess &&
       found == cudaDriverEntryPointSuccess)
     q->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode);
-  ok = ok && q->encode && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
+  ok = ok && cudaMemset(q->status, 0, sizeof(isq::Status)) == cudaSuccess;
   ok = ok && start(&isq::turns_kernel, unsigned(c.head_dim / 2 + 127) / 128, 128, nullptr, q->turns, int(c.head_dim),
                    c.rope_theta, int(c.rope_scaling), c.scale_factor, c.low_freq_factor, c.high_freq_factor,
                    double(c.original_max_position));

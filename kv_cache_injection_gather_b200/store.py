@@ -97,12 +97,13 @@ class FactStore:
         self.device = device
         self.capacity_tokens = capacity_tokens
         self.handle = B.is_store_create(cfg, device)
-        self.query = None
+        # A program that only injects needs no query handle: where there is
+        # none, the calls that do say why.
+        self.query, self._no_query = None, B.IS_OK
         try:
             self.query = B.is_query_create(cfg, device)
-        except B.InjectError:
-            self.close()
-            raise
+        except B.InjectError as e:
+            self._no_query = e.status
 
     # ---- lifetime
     def close(self) -> None:
@@ -300,6 +301,11 @@ class FactStore:
             raise ValueError(f"{name} must be a contiguous bf16 [{self.D}] tensor on cuda:{self.device}")
         return w.data_ptr()
 
+    def _query(self) -> int | None:
+        if self._no_query:
+            raise B.InjectError(self._no_query, "is_query_create")
+        return self.query
+
     def _stream(self, stream: int | None) -> int:
         return _raw_stream(self.device) if stream is None else stream
 
@@ -332,7 +338,7 @@ class FactStore:
             ko = _rows(k_out, "k_out", kr.num_heads, D, T, dev)
         elif k_out is not None or k_weight is not None:
             raise ValueError("k_out and k_weight need k")
-        B.is_query_rotate(self.query, T, _ints(positions, "positions", T, torch.int32, dev), qr, qo,
+        B.is_query_rotate(self._query(), T, _ints(positions, "positions", T, torch.int32, dev), qr, qo,
                           self._weight(q_weight, "q_weight"), kr, ko, self._weight(k_weight, "k_weight"), eps,
                           self._stream(stream))
         return q_out, k_out
@@ -355,7 +361,7 @@ class FactStore:
             qo = _rows(q_out, "q_out", qr.num_heads, D, T, dev)
         elif q_out is not None or q_weight is not None:
             raise ValueError("q_out and q_weight need q")
-        B.is_query_append(self.query, T, _ints(positions, "positions", T, torch.int32, dev),
+        B.is_query_append(self._query(), T, _ints(positions, "positions", T, torch.int32, dev),
                           _ints(slots, "slots", T, torch.int64, dev), kr, vr, self._weight(k_weight, "k_weight"),
                           qr, qo, self._weight(q_weight, "q_weight"), eps, cache, layer, self._stream(stream))
         return q_out
@@ -401,13 +407,14 @@ class FactStore:
                              block_tables.data_ptr(), shared_ptr, shared_len, int(causal),
                              0.0 if scale is None else scale, layer, qr,
                              _rows(out, "out", qr.num_heads, D, T, dev), lse_ptr)
-        need = B.is_query_attend_workspace(self.query, args, cache)
+        query = self._query()
+        need = B.is_query_attend_workspace(query, args, cache)
         work = self._empty((need,), torch.uint8, stream) if need else None
-        B.is_query_attend(self.query, args, cache, None if work is None else work.data_ptr(), need,
+        B.is_query_attend(query, args, cache, None if work is None else work.data_ptr(), need,
                           self._stream(stream))
         return out
 
     def last_query_error(self, stream: int | None = None) -> tuple[int, int]:
         """Waits for the stream; first device-side error of rotate, append
         and attend since the previous call, and its detail."""
-        return B.is_query_last_error(self.query, self._stream(stream))
+        return B.is_query_last_error(self._query(), self._stream(stream))
