@@ -59,6 +59,9 @@ class is_cache_t(ctypes.Structure):
         ("k_cache", _P), ("v_cache", _P), ("layer_stride", _I64), ("block_stride", _I64),
         ("token_stride", _I64), ("head_stride", _I64), ("num_blocks", _I32), ("block_size", _I32),
     ]
+    # (layers, KV heads, head_dim, device) of the tensors that it describes,
+    # where known; not part of the C struct
+    holds = None
 
 
 class is_ipc_handle_t(ctypes.Structure):

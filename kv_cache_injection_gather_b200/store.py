@@ -69,7 +69,11 @@ def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor, head_major: bool = 
         H, blk, hs, ts = a, b, sa, sb
     else:
         blk, H, ts, hs = a, b, sa, sb
-    return B.is_cache_t(k_cache.data_ptr(), v_cache.data_ptr(), ls, bs, ts, hs, nb, blk)
+    if k_cache.get_device() != v_cache.get_device():
+        raise ValueError("K and V caches must be on one device")
+    cache = B.is_cache_t(k_cache.data_ptr(), v_cache.data_ptr(), ls, bs, ts, hs, nb, blk)
+    cache.holds = (L, H, D, k_cache.get_device())
+    return cache
 
 
 class FactStore:
@@ -301,6 +305,14 @@ class FactStore:
             raise ValueError(f"{name} must be a contiguous bf16 [{self.D}] tensor on cuda:{self.device}")
         return w.data_ptr()
 
+    def _check_cache(self, cache: B.is_cache_t, layer: int) -> None:
+        """The kernels reach into the cache by the store's heads and dims."""
+        holds = cache.holds
+        if holds is not None and (layer >= holds[0] or holds[1] < self.H or holds[2] < self.D
+                                  or holds[3] != self.device):
+            raise ValueError(f"a cache of {holds[0]} layers, {holds[1]} KV heads of {holds[2]} on cuda:{holds[3]} does not "
+                             f"hold layer {layer} of {self.H} heads of {self.D} on cuda:{self.device}")
+
     def _query(self) -> int | None:
         if self._no_query:
             raise B.InjectError(self._no_query, "is_query_create")
@@ -352,6 +364,7 @@ class FactStore:
         not stored) of one layer of the paged cache; q (optional) is rotated
         in the same launch and returned in q_out.  Asynchronous."""
         D, T, dev = self.D, k.shape[0], self.device
+        self._check_cache(cache, layer)
         kr, vr = _rows(k, "k", self.H, D, T, dev), _rows(v, "v", self.H, D, T, dev)
         qr = qo = None
         if q is not None:
@@ -381,6 +394,7 @@ class FactStore:
         counts (1 for decode; default: T).  lse, if given, is fp32
         [T][heads].  Asynchronous; last_query_error() has device-side errors."""
         D, T, dev, R = self.D, q.shape[0], self.device, kv_lens.shape[0]
+        self._check_cache(cache, layer)
         if out is None:
             out = self._empty(q.shape, torch.bfloat16, stream)
         if scale is not None and not scale > 0:
