@@ -306,9 +306,10 @@ class FactStore:
         return w.data_ptr()
 
     def _check_cache(self, cache: B.is_cache_t, layer: int) -> None:
-        """The kernels reach into the cache by the store's heads and dims."""
+        """The kernels reach into the cache by the store's heads and dims (a
+        layer that the store lacks is the library's to refuse)."""
         holds = cache.holds
-        if holds is not None and (layer >= holds[0] or holds[1] < self.H or holds[2] < self.D
+        if holds is not None and (holds[0] <= layer < self.L or holds[1] < self.H or holds[2] < self.D
                                   or holds[3] != self.device):
             raise ValueError(f"a cache of {holds[0]} layers, {holds[1]} KV heads of {holds[2]} on cuda:{holds[3]} does not "
                              f"hold layer {layer} of {self.H} heads of {self.D} on cuda:{self.device}")

@@ -58,7 +58,8 @@ def test_a_cache_that_is_too_small_or_elsewhere_is_refused(store, holds, layer):
 
 
 def test_caches_that_hold_the_stores_rows_and_bare_structs_are_taken(store):
-    for cache, layer in ((described(4, 2, 64), 3), (described(1, 2, 64), 0), (described(9, 3, 128), 3), (described(0, 0, 0, known=False), 2)):
+    for cache, layer in ((described(4, 2, 64), 3), (described(1, 2, 64), 0), (described(9, 3, 128), 3),
+                         (described(4, 2, 64), 4), (described(0, 0, 0, known=False), 2)):
         before = store.count()
         for call in calls(store, cache, layer):
             call()
