@@ -11,8 +11,14 @@
 // rows the short one:
 //
 //   S^T = K Q^T   (128 keys x NR, in tensor memory)
-//   P^T = exp2(scale S^T - m), bf16, to shared memory
-//   O^T += V^T P  (D x NR, in tensor memory)
+//   P^T = exp2(scale S^T - m), to shared memory
+//   O^T += V^T P  (D x 2 NR, in tensor memory)
+//
+// P goes in as two bf16 values, itself rounded and the remainder rounded, in
+// columns of their own whose sums are added at the end: together they are
+// within 2^-16 of P, so the result's rounding is the only one that counts.
+// (The tensor cores take both operands in one type; they are 4% busy here, and
+// V is read once for both.)
 //
 // so that a tile costs the softmax threads, one key each, NR values and not a
 // padded 128 (mma.sync over 16-row tiles spent 2900 cycles a warp and 32-key
@@ -47,14 +53,20 @@ struct RowsShape {
   static constexpr int kProductWarp = 4 + kGather;
   static constexpr int kThreads = (4 + kGather + 1) * 32;
   static constexpr int kQBytes = NR * D * 2;
-  static constexpr int kPBytes = NR * kTileKeys * 2;           // twice
+  static constexpr int kPRows = 2 * NR;                        // rounded values, then remainders
+  static constexpr int kPBytes = kPRows * kTileKeys * 2;       // twice
   static constexpr int kJoinBytes = NR * D * 4;                // the cluster's sums of this CTA's dims
+  // Where shared memory has no room for both, the joined sums lie over P: other
+  // CTAs may write them only once this one's products are done.
+  static constexpr bool kJoinOverP = D == 256;
+  static_assert(!kJoinOverP || kJoinBytes <= 2 * kPBytes, "the joined sums fit over P");
   static constexpr int kRingBytes = kSlots * kSlotBytes;
-  static constexpr int kSmemBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024 + 2 * kPBytes + kJoinBytes + 1024;
-  static constexpr int kGroups = (D + 127) / 128;              // O^T accumulators
+  static constexpr int kSmemBytes = kRingBytes + (kQBytes + 1023) / 1024 * 1024 + 2 * kPBytes +
+                                    (kJoinOverP ? 0 : kJoinBytes) + 1024;
+  static constexpr int kGroups = (D + 127) / 128;              // O^T accumulators, of kPRows columns
   // S^T twice and O^T, as a power of two of columns
-  static constexpr int kColumns = NR == 16 ? 64 : 128;
-  static_assert((2 + kGroups) * NR <= kColumns, "tensor memory");
+  static constexpr int kColumns = 2 * NR + kGroups * kPRows <= 64 ? 64 : 128;
+  static_assert(2 * NR + kGroups * kPRows <= kColumns, "tensor memory");
 };
 
 template <int D, int NR>
@@ -86,7 +98,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
     wait_for_previous();
     return;
   }
-  if (a.splits > 1) cluster_arrive();  // this CTA has started: its shared memory may be written
+  // this CTA has started: its shared memory may be written
+  if (!S::kJoinOverP && a.splits > 1) cluster_arrive();
   // what needs no metadata first, a barrier a thread
   if (tid < NS) {
     bar_init(&bar_full[tid], 1);
@@ -111,7 +124,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   find_unit<NR, NT>(a, int32_t(unit), r, tile, rq);
   if (r < 0) {  // so for the whole cluster
     if (warp == S::kProductWarp) tmem_free(s_tmem, S::kColumns);
-    if (a.splits > 1) cluster_wait();
+    if (!S::kJoinOverP && a.splits > 1) cluster_wait();
     wait_for_previous();  // on every path: the next grid relies on both
     return;
   }
@@ -134,8 +147,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* p_tiles = ring + S::kRingBytes;
-  float* join_o = reinterpret_cast<float*>(p_tiles + 2 * S::kPBytes);  // [split][row][D / splits]
-  unsigned char* q_tile = p_tiles + 2 * S::kPBytes + S::kJoinBytes;
+  float* join_o = reinterpret_cast<float*>(p_tiles + (S::kJoinOverP ? 0 : 2 * S::kPBytes));  // [split][row][D / splits]
+  unsigned char* q_tile = p_tiles + 2 * S::kPBytes + (S::kJoinOverP ? 0 : S::kJoinBytes);
 
   if (tid < NR) {
     s_lim[tid] = tid < rows ? min(hi, row_limit(a, rq, token_of(tid))) : hi;
@@ -149,7 +162,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;               // S^T, twice NR columns
-  const uint32_t tmem_o = tmem + 2 * NR;      // O^T, NR columns per 128 dims
+  const uint32_t tmem_o = tmem + 2 * NR;      // O^T, kPRows columns per 128 dims
 
   if (warp >= 4 && warp < S::kProductWarp) {
     gather_tiles<D, NS, S::kGather>(a, &k_map, &v_map, warp - 4, r, h, lo, hi, tiles, ring, bar_full, bar_empty, nullptr,
@@ -187,8 +200,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 #pragma unroll
           for (int k = 0; k < kTileKeys / 16; ++k)
             // V^T: 128 rows of dims; with D below 128 its slabs repeat (lead 0)
-            mma_ss(tmem_o + g * NR, operand<D>(va + g * 2 * kSlabStep + k * (D * 32), D < 128 ? 0 : kSlabStep),
-                   operand<128>(pa + dims_at<128>(k), 16), product(NR, true, false), t > 0 || k > 0);
+            mma_ss(tmem_o + g * S::kPRows, operand<D>(va + g * 2 * kSlabStep + k * (D * 32), D < 128 ? 0 : kSlabStep),
+                   operand<128>(pa + dims_at<128>(k), 16), product(S::kPRows, true, false), t > 0 || k > 0);
         tc_commit(&bar_empty[slot]);
         tc_commit(&bar_o);
       }
@@ -294,7 +307,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 #pragma unroll
           for (int c = 0; c < NR; ++c) l[c] *= shrink[c];
 #pragma unroll
-          for (int g = 0; g < S::kGroups; ++g) {
+          for (int g = 0; g < 2 * S::kGroups; ++g) {
             tmem_ld<NR>(tmem_o + g * NR + lanes, v);
             tmem_wait_ld();
 #pragma unroll
@@ -304,9 +317,9 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
           tmem_wait_st();
         }
       }
-      // P^T as the second product's B operand: a tile of [row][128 keys].
-      // The probabilities are rounded to bf16: V, the other operand, is no
-      // finer, and the sum l keeps them in fp32.
+      // P^T as the second product's B operand: a tile of [row][128 keys], the
+      // rows' values rounded to bf16 and, NR rows on, what that left out (the
+      // difference is exact).
       unsigned char* p = p_tiles + (t & 1) * S::kPBytes + (tid & 7) * 2;
 #pragma unroll
       for (int c = 0; c < NR; c += 4) {
@@ -317,8 +330,10 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
         for (int i = 0; i < 4; ++i) {
           const float e = exp2_fast(x[c + i] - (m[i] == neg_inf() ? 0.f : m[i]));  // no key seen yet: every term is 0
           l[c + i] += e;
-          *reinterpret_cast<uint16_t*>(p + tile_at<128>(c + i, tid >> 3)) =
-              __bfloat16_as_ushort(__float2bfloat16_rn(e));
+          const __nv_bfloat16 near = __float2bfloat16_rn(e);
+          const __nv_bfloat16 rest = __float2bfloat16_rn(e - __bfloat162float(near));
+          *reinterpret_cast<uint16_t*>(p + tile_at<128>(c + i, tid >> 3)) = __bfloat16_as_ushort(near);
+          *reinterpret_cast<uint16_t*>(p + tile_at<128>(NR + c + i, tid >> 3)) = __bfloat16_as_ushort(rest);
         }
       }
       proxy_fence();
@@ -348,8 +363,13 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 #pragma unroll
     for (int g = 0; g < S::kGroups; ++g) {
       if (tiles > 0) {
-        tmem_ld<NR>(tmem_o + g * NR + (uint32_t(warp) << 21), o[g]);
+        uint32_t rest[NR];
+        tmem_ld<NR>(tmem_o + g * S::kPRows + (uint32_t(warp) << 21), o[g]);
+        tmem_ld<NR>(tmem_o + g * S::kPRows + NR + (uint32_t(warp) << 21), rest);
         tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < NR; ++c)
+          o[g][c] = __float_as_uint(__uint_as_float(o[g][c]) + __uint_as_float(rest[c]));
       } else {
 #pragma unroll
         for (int c = 0; c < NR; ++c) o[g][c] = 0;
@@ -369,7 +389,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 
   // ---- join the splits: CTA k of the cluster gets everybody's maxima and sums
   // and the k-th share of the dims, written into its shared memory
-  if (a.splits > 1) cluster_wait();  // they have all started
+  if (S::kJoinOverP && a.splits > 1) cluster_arrive();  // this CTA's products are done
+  if (a.splits > 1) cluster_wait();  // so are all CTAs', or they have all started
   constexpr int kLogD = D == 256 ? 8 : D == 128 ? 7 : D == 64 ? 6 : 5;
   const int share_log2 = kLogD - a.splits_log2, share = 1 << share_log2;
   const uint32_t o_at = smem_addr(join_o), ml_at = smem_addr(s_join_ml);
