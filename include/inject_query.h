@@ -113,10 +113,9 @@ int is_query_append(is_query_t* query, int32_t num_tokens, const int32_t* positi
  * is allowed: that block's first part comes from the shared list).  Query
  * head h reads KV head h / (num_q_heads / num_kv_heads):
  *   out[t][h] = bf16_rne(sum_j p_j v_j),  p = softmax_j(scale q . k_j)
- * in fp32.  For up to 16 rows (queries x query heads) a KV head and request, and
- * for every call with head_dim 32 or 256, the probabilities meet v as sums of
- * two bf16 values, within 2^-16 of them; for more rows, and for a shared prefix
- * that is attended to once for the batch, rounded to bf16.
+ * in fp32.  The probabilities meet v as sums of two bf16 values, within 2^-16
+ * of them, or, with head_dim 64 or 128 and more than 16 rows (queries x query
+ * heads of a KV head; by max_q_len), rounded to bf16.
  * A query that sees no key, or none with a score above -inf, gets zeros and
  * lse -inf.  NaN and infinities in cache elements that a query does not see do
  * not reach it (its sum may then run in another order). */

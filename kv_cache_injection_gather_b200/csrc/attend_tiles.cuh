@@ -7,7 +7,7 @@
 // that share a KV head -- and walks its keys in tiles of 128:
 //
 //   S = Q K^T (128 x 128, fp32 in tensor memory)
-//   P = exp2(scale S - m), rounded to bf16, over S in tensor memory
+//   P = exp2(scale S - m), in bf16, over S in tensor memory
 //   O += P V
 //
 // Two streams keep the tensor cores busy while a stream's softmax runs.  A
@@ -159,6 +159,14 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
     const __grid_constant__ CUtensorMap v_map) {
   using S = TilesShape<D>;
   constexpr int CPR = D / 8, NS = S::kSlots;
+  // P meets V rounded to bf16, as the tensor cores take both operands in one
+  // type: an error of up to 2^-8 of sum p |v| beside the result's rounding.  For
+  // a prefix (decode) the remainder of the rounding goes in as well, behind P in
+  // the scores' columns, and P is good to 2^-16: 100 requests behind 4096 shared
+  // tokens 168 -> 171 us, behind 16384 134 -> 140.  Where the products bound the
+  // call it would cost a fifth (100 requests of 16-64 queries 381 -> 463 us, two
+  // prompts of 4096 tokens 282-315 -> 330-366), so there it stays rounded.
+  constexpr bool kRest = SHARED;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2][2], bar_p[2][2], bar_o[2][2],
       bar_end[2], bar_edge;
@@ -311,6 +319,11 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
           for (int k = 0; k < 4; ++k)
             mma_ts(to, ts + half * 64 + k * 8, vd + k * (D * 32 / 16), product(D, false, true),
                    i > 0 || half > 0 || k > 0);
+          if constexpr (kRest) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(to, ts + half * 64 + 32 + k * 8, vd + k * (D * 32 / 16), product(D, false, true), true);
+          }
           tc_commit(&bar_o[st][half]);
           if (half == 1) free_slot(slot + 1);
           // (the next scores overwrite the probabilities that these products
@@ -410,6 +423,7 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
+          [[maybe_unused]] uint32_t rest[16];  // kRest: what the rounding left out (exact)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int at = c * 32 + 2 * i;
@@ -423,8 +437,10 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
             }
             sum2 = add2(sum2, e);
             p[i] = to_bf16x2(e);
+            if constexpr (kRest) rest[i] = to_bf16x2(fma2(from_bf16x2(p[i]), two(-1.f, -1.f), e));
           }
           tmem_st16(tp + c * 16, p);
+          if constexpr (kRest) tmem_st16(tp + 32 + c * 16, rest);
         }
         tmem_wait_st();
         tc_fence_before();

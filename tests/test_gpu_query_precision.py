@@ -11,10 +11,10 @@ from test_gpu_query import make, pkg, within  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-def fine_tolerance(c, causal, scale=None):
+def fine_tolerance(c, causal, scale=None, polynomial=0.0):
     """The bound of query_cases.attend_reference without its term for
-    probabilities rounded to bf16 (2^-8 A) and for the polynomial (2^-17 A),
-    which attend_rows has neither of:
+    probabilities rounded to bf16 (2^-8 A) and, but for a prefix with a grid of
+    its own, for exponentials by a polynomial (2^-17 A):
 
       * the result's own rounding: 2^-8 |out|;
       * a probability p as the sum of two bf16 values, p rounded and the
@@ -45,7 +45,7 @@ def fine_tolerance(c, causal, scale=None):
             e = 2.0 ** -24 * (D + 2) * S + 2.0 ** -22 * (s.abs().amax(-1) + 2)
             A = torch.einsum("hgn,nhd->hgd", torch.softmax(s, -1), V[:lim].abs())
             tol[t] = (2.0 ** -8 * out[t].view(H, G, D).abs()
-                      + A * (2.0 ** -16 + 4 * e[..., None] + 4 * lim * 2.0 ** -24)).reshape(H * G, D)
+                      + A * (2.0 ** -16 + polynomial + 4 * e[..., None] + 4 * lim * 2.0 ** -24)).reshape(H * G, D)
     return out, tol
 
 
@@ -80,6 +80,28 @@ def test_values_that_cancel(pkg, D):  # noqa: F811
     c.sync_cache()
     out, tol = fine_tolerance(c, True)
     with make(pkg, D, 2) as s:
+        got = c.call(s, pkg.cache_desc(c.k_cache, c.v_cache))
+        assert s.last_query_error() == (0, 0)
+    within(got, out, tol)
+
+
+@pytest.mark.parametrize("D,shared,block", [(64, 520, 16), (128, 260, 16), (128, 275, 24)])
+def test_decode_behind_a_prefix_at_the_results_precision(pkg, D, shared, block):  # noqa: F811
+    """A prefix that has a grid of its own, by its bytes, in which four keys
+    carry nearly all weight, nearly equally, with values that cancel."""
+    R, H, G = 64, 8, 4
+    assert shared * R * H * D * 4 >= 64 << 20
+    c = Paged(460 + D, D, H, G, block, [1] * R, [r % 7 for r in range(R)], shared=shared)
+    c.q.mul_(0.25)
+    c.q[..., 0] = 8
+    c.k[..., 0] = -80 / math.sqrt(D)  # e^-7 of the weight
+    for i, j in enumerate((3, 50, 131, 200)):
+        b, o = int(c.shared_blocks[j // block]), j % block
+        c.k[b, o, :, 0] = 0
+        c.v[b, o] += 100 * (-1) ** i
+    c.sync_cache()
+    out, tol = fine_tolerance(c, True, polynomial=2.0 ** -17)
+    with make(pkg, D, H) as s:
         got = c.call(s, pkg.cache_desc(c.k_cache, c.v_cache))
         assert s.last_query_error() == (0, 0)
     within(got, out, tol)
