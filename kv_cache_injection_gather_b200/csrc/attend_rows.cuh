@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
   const int32_t end = row_limit(a, rq, token_of(rows - 1));
   const uint32_t all_tiles = end > a.first_key ? uint32_t(end - begin + kTileKeys - 1) / kTileKeys : 0;
   const uint32_t shares = a.key_parts << a.splits_log2, mine = (part << a.splits_log2) + split;
-  // (up to 2^24 tiles, times fewer than 2^8 shares)
+  // (below 2^24 tiles, times up to 2^8 shares)
   const int32_t lo = begin + int32_t(all_tiles * mine / shares) * kTileKeys;
   const uint32_t last = all_tiles * (mine + 1) / shares;
   const int32_t hi = all_tiles == 0 ? lo : last == all_tiles ? end : begin + int32_t(last) * kTileKeys;

@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(TilesShape<D>::kThreads, 1) attend_tiles_kerne
   };
   // keys [lo, hi) of this CTA: whole tiles but the last
   const int32_t all = SHARED ? a.shared_len : limit_of(rows - 1);
-  const uint32_t all_tiles = (uint32_t(all) + kTileKeys - 1) / kTileKeys;  // up to 2^24, times up to 16 splits
+  // (below 2^24 tiles, times up to 32 splits)
+  const uint32_t all_tiles = (uint32_t(all) + kTileKeys - 1) / kTileKeys;
   const int32_t lo = int32_t(all_tiles * split / a.splits) * kTileKeys;
   const uint32_t last = all_tiles * (split + 1) / a.splits;
   const int32_t hi = last == all_tiles ? all : int32_t(last) * kTileKeys;

@@ -152,6 +152,11 @@ constexpr int64_t kSharedBytes = 64 << 20;
 constexpr int kTilesPerPart = 8;
 constexpr int kMostPrefixParts = 16;
 constexpr int kMostParts = 32;  // a lane each in join_parts
+// A unit's tiles times its shares are counted in 32 bits (attend_tiles: parts;
+// attend_rows: CTAs of a cluster times parts).
+static_assert((int64_t(isq::kMostKeys) / isq::kTileKeys + 1) * std::max(kMostParts, kMostPrefixParts) * isq::kMostSplits <=
+                  int64_t(1) << 32,
+              "tile numbers");
 
 // Fills in the clusters of 2^i CTAs that run at once, as ask(CTAs, number)
 // says: one CTA an SM, but a cluster's in one GPC, so a part of a GPU may have
