@@ -114,8 +114,8 @@ int is_query_append(is_query_t* query, int32_t num_tokens, const int32_t* positi
  * head h reads KV head h / (num_q_heads / num_kv_heads):
  *   out[t][h] = bf16_rne(sum_j p_j v_j),  p = softmax_j(scale q . k_j)
  * in fp32.  The probabilities meet v as sums of two bf16 values, within 2^-16
- * of them, or, with head_dim 64 or 128 and more than 16 rows (queries x query
- * heads of a KV head; by max_q_len), rounded to bf16.
+ * of them, for up to 16 rows (max_q_len queries x query heads of a KV head) and
+ * with head_dim 256; for more rows with head_dim 32, 64 or 128 rounded to bf16.
  * A query that sees no key, or none with a score above -inf, gets zeros and
  * lse -inf.  NaN and infinities in cache elements that a query does not see do
  * not reach it (its sum may then run in another order). */

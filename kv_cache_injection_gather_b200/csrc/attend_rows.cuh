@@ -12,13 +12,16 @@
 //
 //   S^T = K Q^T   (128 keys x NR, in tensor memory)
 //   P^T = exp2(scale S^T - m), to shared memory
-//   O^T += V^T P  (D x 2 NR, in tensor memory)
+//   O^T += V^T P  (D x NR or D x 2 NR, in tensor memory)
 //
-// P goes in as two bf16 values, itself rounded and the remainder rounded, in
-// columns of their own whose sums are added at the end: together they are
-// within 2^-16 of P, so the result's rounding is the only one that counts.
-// (The tensor cores take both operands in one type; they are 4% busy here, and
-// V is read once for both.)
+// The tensor cores take both operands in one type, so P is rounded to bf16: by
+// itself an error of up to 2^-8 of sum p |v| beside the result's rounding.  For
+// units of 16 rows the remainder of the rounding goes in as well, in columns of
+// its own (V is read once for both) whose sums are added at the end.  Together
+// they are within 2^-16 of P, and the result's rounding is the only one that
+// counts; the tensor cores are 4% busy and decode takes 0-2% longer for it.
+// Units of 32 rows (prompts with head_dim 32) would take a fifth longer (one of
+// 2048 tokens 300 -> 353 us); they keep the rounded P.
 //
 // so that a tile costs the softmax threads, one key each, NR values and not a
 // padded 128 (mma.sync over 16-row tiles spent 2900 cycles a warp and 32-key
@@ -53,7 +56,8 @@ struct RowsShape {
   static constexpr int kProductWarp = 4 + kGather;
   static constexpr int kThreads = (4 + kGather + 1) * 32;
   static constexpr int kQBytes = NR * D * 2;
-  static constexpr int kPRows = 2 * NR;                        // rounded values, then remainders
+  static constexpr bool kRest = NR == 16;
+  static constexpr int kPRows = kRest ? 2 * NR : NR;           // rounded values, then remainders
   static constexpr int kPBytes = kPRows * kTileKeys * 2;       // twice
   static constexpr int kJoinBytes = NR * D * 4;                // the cluster's sums of this CTA's dims
   // Where shared memory has no room for both, the joined sums lie over P: other
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 #pragma unroll
           for (int c = 0; c < NR; ++c) l[c] *= shrink[c];
 #pragma unroll
-          for (int g = 0; g < 2 * S::kGroups; ++g) {
+          for (int g = 0; g < S::kGroups * S::kPRows / NR; ++g) {
             tmem_ld<NR>(tmem_o + g * NR + lanes, v);
             tmem_wait_ld();
 #pragma unroll
@@ -318,8 +322,8 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
         }
       }
       // P^T as the second product's B operand: a tile of [row][128 keys], the
-      // rows' values rounded to bf16 and, NR rows on, what that left out (the
-      // difference is exact).
+      // rows' values rounded to bf16 and, NR rows on, what that left out (kRest;
+      // the difference is exact).
       unsigned char* p = p_tiles + (t & 1) * S::kPBytes + (tid & 7) * 2;
 #pragma unroll
       for (int c = 0; c < NR; c += 4) {
@@ -331,9 +335,10 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
           const float e = exp2_fast(x[c + i] - (m[i] == neg_inf() ? 0.f : m[i]));  // no key seen yet: every term is 0
           l[c + i] += e;
           const __nv_bfloat16 near = __float2bfloat16_rn(e);
-          const __nv_bfloat16 rest = __float2bfloat16_rn(e - __bfloat162float(near));
           *reinterpret_cast<uint16_t*>(p + tile_at<128>(c + i, tid >> 3)) = __bfloat16_as_ushort(near);
-          *reinterpret_cast<uint16_t*>(p + tile_at<128>(NR + c + i, tid >> 3)) = __bfloat16_as_ushort(rest);
+          if constexpr (S::kRest)
+            *reinterpret_cast<uint16_t*>(p + tile_at<128>(NR + c + i, tid >> 3)) =
+                __bfloat16_as_ushort(__float2bfloat16_rn(e - __bfloat162float(near)));
         }
       }
       proxy_fence();
@@ -363,13 +368,16 @@ __global__ void __launch_bounds__(RowsShape<D, NR>::kThreads, 1) attend_rows_ker
 #pragma unroll
     for (int g = 0; g < S::kGroups; ++g) {
       if (tiles > 0) {
-        uint32_t rest[NR];
         tmem_ld<NR>(tmem_o + g * S::kPRows + (uint32_t(warp) << 21), o[g]);
-        tmem_ld<NR>(tmem_o + g * S::kPRows + NR + (uint32_t(warp) << 21), rest);
-        tmem_wait_ld();
+        if constexpr (S::kRest) {
+          uint32_t rest[NR];
+          tmem_ld<NR>(tmem_o + g * S::kPRows + NR + (uint32_t(warp) << 21), rest);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < NR; ++c)
-          o[g][c] = __float_as_uint(__uint_as_float(o[g][c]) + __uint_as_float(rest[c]));
+          for (int c = 0; c < NR; ++c)
+            o[g][c] = __float_as_uint(__uint_as_float(o[g][c]) + __uint_as_float(rest[c]));
+        }
+        tmem_wait_ld();
       } else {
 #pragma unroll
         for (int c = 0; c < NR; ++c) o[g][c] = 0;
