@@ -123,7 +123,10 @@ typedef struct {
   int32_t num_tokens;            /* rows of q, out and lse                     */
   int32_t num_requests;
   int32_t max_q_len;             /* >= every n_r (decides the launch shape)    */
-  int32_t max_blocks_per_req;    /* row length of block_tables                 */
+  int32_t max_blocks_per_req;    /* row length of block_tables (bounds the keys
+                                    and so decides the launch shape: rows far
+                                    wider than the lengths cost a few requests
+                                    some 4 us for a second grid)               */
   const int32_t* q_offsets;      /* device [num_requests + 1], non-decreasing  */
   const int32_t* start_pos;      /* device [num_requests]                      */
   const int32_t* kv_lens;        /* device [num_requests]                      */

@@ -19,7 +19,7 @@
 // units of 16 rows the remainder of the rounding goes in as well, in columns of
 // its own (V is read once for both) whose sums are added at the end.  Together
 // they are within 2^-16 of P, and the result's rounding is the only one that
-// counts; the tensor cores are 4% busy and decode takes 0-2% longer for it.
+// counts; the tensor cores are 7% busy and decode takes 0-3% longer for it.
 // Units of 32 rows (prompts with head_dim 32) would take a fifth longer (one of
 // 2048 tokens 300 -> 353 us); they keep the rounded P.
 //
@@ -33,12 +33,16 @@
 // and long ones over several clusters, whose sums a grid behind joins.
 //
 // Measured on B200 (32 query and 8 KV heads of 128, block 16): 100 requests of
-// 800-3200 keys 141 us, 5.8 TB/s of keys and values, 0.90 of the copy
+// 800-3200 keys 143 us, 5.7 TB/s of keys and values, 0.89 of the copy
 // bandwidth; 3 requests of 60-131 k keys (4 KV heads, 12 parts: 144 of 148 SMs)
-// 114 us, 5.5 TB/s, as the longest one's parts end last.  A tile costs an SM
-// some 1500 cycles, of 2200 that its share of the bandwidth leaves; a unit's
-// start and end cost some 10 000, which is what bounds requests of a few hundred
-// keys (100 of 550: 70 us, 3.3 TB/s).
+// 117 us, 5.4 TB/s, as the longest one's parts end last.  A tile's rounded
+// probabilities alone cost an SM some 1500 cycles, of 2200 that its share of the
+// bandwidth leaves; a unit's start and end cost some 10 000, which is what bounds
+// requests of a few hundred keys (100 of 550: 78 us, 2.9 TB/s).  With head_dim 32,
+// 64 and 256 the 100 requests of 800-3200 keys take 109, 115 and 346 us (0.29,
+// 0.55 and 0.74 of the copy bandwidth): a unit's start and end again, and at 256 a
+// ring of three tiles.  Key by key (blocks of 5, 4, 1 tokens) they take 219, 228
+// and 242 us, as a gather warp waits for each tile that it brings.
 #pragma once
 
 #include "attend_common.cuh"

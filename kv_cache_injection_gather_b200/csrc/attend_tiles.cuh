@@ -28,10 +28,11 @@
 // the next tile's scores.
 //
 // Measured on B200 (32 query and 8 KV heads of 128): two causal prompts of
-// 4096 tokens 280-310 us (870-960 TFLOP/s, 0.52-0.57 of the burst bf16 GEMM;
+// 4096 tokens 280-315 us (850-960 TFLOP/s, 0.51-0.58 of the burst bf16 GEMM;
 // the spread is the card's power limit), 100 requests of 16-64 queries over
-// 3300-5000 keys 385 us (690 TFLOP/s of what is not masked or padded); with a
-// tile as one piece 303-328 and 412 us.  A tile of both streams takes 3400
+// 3300-5000 keys 382 us (690 TFLOP/s of what is not masked or padded) on a cool
+// card, 435 (610) on one that is warm from other products; with a tile as one
+// piece 303-328 and 412 us.  A tile of both streams takes 3400
 // cycles.  Its halves alternate between softmax (maximum 300, exponentials
 // 1100, 770 of which the special-function units take for both streams) and
 // products (both streams' 1300, as scores of 64 keys read more shared memory
@@ -54,9 +55,9 @@ template <int D>
 struct TilesShape {
   static constexpr int kSlotBytes = kTileKeys * D * 2;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 4 : 8;
-  // 12 warps, as that leaves a thread 168 registers to run ahead with (100
-  // requests of 16-64 queries: with 4 gather warps 396 us, 2: 385, 1: 476).  One
-  // warp a stream issues its products: a wait costs a lone thread some 200
+  // By time: 100 requests of 16-64 queries with 4 gather warps 396 us, 2: 385, 1:
+  // 476.  (Registers do not decide it: a thread uses 125 of the 168 that 12 warps
+  // leave, and 14 warps would leave 144.)  One warp a stream issues its products: a wait costs a lone thread some 200
   // cycles of latency, and a tile has four.
   static constexpr int kGather = 2;
   static constexpr int kProductWarp = 8 + kGather;       // and the next

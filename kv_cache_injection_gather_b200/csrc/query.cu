@@ -143,12 +143,23 @@ constexpr int kKeysPerRowPart = 256;
 constexpr int kKeysSpared = 1536;
 constexpr int kKeysSparedFull = 3000;
 // The shared prefix gets a grid of its own (attend_tiles over all requests'
-// rows) where the requests would otherwise read this many bytes of it.
+// rows) where the requests would otherwise read this many bytes of it.  Decode,
+// 4 queries a KV head, 100 own keys; with this grid against without it, us:
+//                 8 k shared                       131 k shared
+//   KV heads      1        2        4        8     1        2        4         8
+//   2 requests    -        -        -        -     97/31    102/43   105/66    116/114
+//   8 requests    -      23/25    25/25    25/39  100/66   104/113   106/234   119/454
+//   64 requests  35/39    37/66    48/127   71/248 158/453  160/891   177/1719  215/3394
+// So bytes alone are too simple a rule for a few requests with few KV heads
+// behind a very long prefix: kMostPrefixParts leaves SMs without work there, and
+// the grid costs up to 3 times what the requests' own would.
 constexpr int64_t kSharedBytes = 64 << 20;
 // Its keys are split into parts of this many tiles, as few CTAs as that: they
 // run beside the requests' grid, which is short of bandwidth and not of SMs
 // (100 requests of 2000 keys behind 4096 shared: 171 us; with parts of 2 tiles,
-// which take every SM first, 187; of 16, which end last, 192).
+// which take every SM first, 187; of 16, which end last, 192).  The requests'
+// grid reads every part's sums again for each row, so they are kept few; other
+// bounds than 16 were not measured.
 constexpr int kTilesPerPart = 8;
 constexpr int kMostPrefixParts = 16;
 constexpr int kMostParts = 32;  // a lane each in join_parts

@@ -8,9 +8,10 @@
 // a few operations an element: HBM bandwidth bounds long batches, the latency
 // of a launch and of two dependent loads short ones.  Measured on B200 (32
 // query and 8 KV heads of 128): append of 16384 tokens 63.5 us, 0.98 of the copy
-// bandwidth; rotate of 16384 tokens with norm 59.5 us, 0.87 (128 registers a
-// thread leave 16 warps an SM, and the norm's shuffles stand between load and
-// store); up to 300 tokens 4.2 us.
+// bandwidth; rotate of 16384 tokens with norm 60 us, 0.87 (128 registers a
+// thread, as the launch bound of 512 threads leaves them, make 16 warps an SM,
+// the norm's shuffles stand between load and store, and the kernels with a norm
+// spill 48 to 64 bytes a thread under that bound); up to 300 tokens 4.2 us.
 #pragma once
 
 #include <cuda_bf16.h>

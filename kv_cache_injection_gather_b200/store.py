@@ -430,6 +430,7 @@ class FactStore:
         return out
 
     def last_query_error(self, stream: int | None = None) -> tuple[int, int]:
-        """Waits for the stream; first device-side error of rotate, append
-        and attend since the previous call, and its detail."""
+        """Waits for the stream (and no other); first device-side error of
+        rotate, append and attend recorded since the previous call, and its
+        detail."""
         return B.is_query_last_error(self._query(), self._stream(stream))
